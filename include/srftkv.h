@@ -50,7 +50,7 @@
  *    owned by the caller; the library allocates no device memory.  State it
  *    keeps between calls: per-device capability checks, a per-host-thread
  *    copy of the last sign vector and error message, constant twiddle tables
- *    compiled into the kernels, two device fault words (one per kernel
+ *    compiled into the kernels, four device fault words (one per kernel
  *    family) and the fixed-size scratch array of
  *    q4kv_decode_attention_static (all file-scope __device__ data, held by
  *    every GPU that loads the library), and the two process-wide poll
@@ -274,6 +274,123 @@ int srft_transform(const void* x, float* y, int n, int d, uint64_t sign_seed, in
 int srht_transform(const void* x, float* y, int n, int d, uint64_t sign_seed, int inverse,
                    void* stream);
 
+/* ------------------------------------------------------------------------
+ * The paged cache: tokens of many sequences in fixed-size pages.
+ *
+ * The calls above address a cache by one (outer, t_offset) window.  A serving
+ * program appends to many sequences of different lengths at once and grows
+ * them in pages; these three calls write K and V rows wherever their slot is,
+ * read them back from there, and attend over a sequence's pages with any
+ * number of query tokens (one, a few drafted ones, a chunk of a prompt, a
+ * whole prompt), in the model's 16-bit type.  (The method's pages write of
+ * the codec and of tiled attention only; pages, slots and causal chunks are
+ * the library's.)  The encoding of a row is that of srft_kv_quantize: the
+ * same rotation, lambda, group scales and codes.
+ * ------------------------------------------------------------------------ */
+
+#define SRFTKV_DTYPE_FP16 0 /* IEEE half rows */
+#define SRFTKV_DTYPE_BF16 1 /* bfloat16 rows */
+
+/*
+ * One side (K or V) of the pages of one layer, a pool that all sequences share:
+ *   codes  : uint8 [n_pages][H][page_size][d*bits/8]   (16-byte aligned)
+ *   scales : [n_pages][H][page_size][d/group], element type per scale_format
+ *            (16-byte aligned)
+ * Slot s of the pool is row s % page_size of page s / page_size.
+ * d in {64, 128, 256}; group a power of two with 16 <= group <= d; page_size a
+ * power of two with 16 <= page_size <= 256; bits 4 or 8.
+ */
+typedef struct srftkv_pages {
+    void* codes;
+    void* scales;
+    const float* lambda; /* fp32 [H][d] > 0, 16-byte aligned; NULL means all ones */
+    int n_pages, H, page_size, d, group;
+    int bits;         /* 4 or 8 */
+    int transform;    /* SRFTKV_TRANSFORM_* */
+    int scale_format; /* SRFTKV_SCALE_* */
+} srftkv_pages;
+
+/*
+ * srft_kv_quantize_paged -- encode rows into their slots.
+ *   xk, xv  : rows [n_tokens][H][d] of `dtype` (fp16 or bf16), token t's H*d
+ *             values at x + t * stride (strides in elements, multiples of 8, 0
+ *             means H*d; a slice of a fused projection's output needs no copy);
+ *             16-byte aligned
+ *   slots   : device int64 [n_tokens], the slot of each token in both pools.
+ *             A negative slot skips its token (padding).  A slot at or past
+ *             n_pages * page_size is skipped too and sets bit 16 of the fault
+ *             word.  Slots of one call must differ: where two tokens share one,
+ *             that slot's row may mix the two.
+ * k or v may be NULL (its rows are then ignored); both sides share all sizes
+ * (n_pages, H, page_size, d, group).  n_tokens == 0 is a no-op.  Rows of the
+ * pools that no slot names are not written.
+ */
+int srft_kv_quantize_paged(const srftkv_pages* k, const void* xk, int64_t xk_stride, const srftkv_pages* v,
+                           const void* xv, int64_t xv_stride, const int64_t* slots, int n_tokens, int dtype,
+                           uint64_t sign_seed, void* stream);
+
+/*
+ * srft_kv_dequantize_paged -- decode the rows of `slots` to xk, xv (same
+ * layout and strides as above, written).  Output rows whose slot is negative
+ * or outside the pool are left as they were (outside: fault bit 16 as above);
+ * the same slot may appear any number of times.
+ */
+int srft_kv_dequantize_paged(const srftkv_pages* k, void* xk, int64_t xk_stride, const srftkv_pages* v, void* xv,
+                             int64_t xv_stride, const int64_t* slots, int n_tokens, int dtype, uint64_t sign_seed,
+                             void* stream);
+
+/*
+ * The sequences of an attention call.  Sequence b has seq_lens[b] cached tokens
+ * (the query tokens' own K and V among them), token t in row t % page_size of
+ * page block_table[b][t / page_size], and the query rows cu_q[b] ..
+ * cu_q[b+1]-1, which are its last tokens: query i of m sits at position
+ * seq_lens[b] - m + i.  The three arrays are device int32 and are read by the
+ * kernels only, so a captured call may be replayed after they change within
+ * the bounds below.
+ */
+typedef struct srftkv_paged_batch {
+    const int32_t* block_table; /* [B][max_pages]; entries past a sequence's last page are not read */
+    const int32_t* seq_lens;    /* [B] */
+    const int32_t* cu_q;        /* [B+1], ascending from 0 to at most total_q; NULL: one query token a sequence */
+    int B, max_pages;
+    int total_q;                /* rows of q and out */
+    int max_q;                  /* upper bound of cu_q[b+1] - cu_q[b] */
+    int max_seq_len;            /* upper bound of seq_lens[b]; 0 means max_pages * page_size */
+} srftkv_paged_batch;
+
+/*
+ * q4kv_paged_attention -- causal attention of the query rows over the pages.
+ *   q, out : [total_q][Hq][d] of `dtype`, strides in elements between tokens
+ *            (multiples of 8, 0 means Hq*d), 16-byte aligned; they may not overlap
+ *   out[i][h] = sum_t softmax_t(sm_scale * q . k_hat_t) v_hat_t over the cached
+ *            tokens t <= position of i, and with window > 0 only those with
+ *            t > position - window; query head h reads kv head h / (Hq/H).
+ *            A query that sees no token (seq_lens[b] == 0, or more query
+ *            rows than cached tokens) gets zeros.  Rows of out at or past
+ *            cu_q[B] are left as they were.
+ *   k, v   : both sides, sharing all sizes and the scale format
+ *   sm_scale: <= 0 selects 1/sqrt(d)
+ *   workspace: device scratch of q4kv_paged_attention_workspace_size(...)
+ *            bytes, 16-byte aligned, uninitialised; calls that may run at the
+ *            same time need one each
+ * seq_lens[b] is clamped to [0, min(max_seq_len, max_pages * page_size)] and a
+ * sequence's query count to max_q (rows past it are left as they were).  A
+ * block-table entry outside [0, n_pages) reads no memory outside the pools: its
+ * tokens count as rows of zeros and bit 17 of the fault word is set.
+ * Requires Hq % H == 0, Hq / H <= 128, total_q * Hq < 2^31.
+ * Values code * scale (lambda times the rotated row) are formed in fp16 where
+ * they enter the tensor cores: they must stay below 65504 in size, and those
+ * below 2^-14 keep fewer than 11 bits.
+ */
+int q4kv_paged_attention(const void* q, int64_t q_stride, void* out, int64_t out_stride, int dtype, int Hq,
+                         const srftkv_pages* k, const srftkv_pages* v, const srftkv_paged_batch* batch, float sm_scale,
+                         int window, uint64_t sign_seed, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace q4kv_paged_attention needs on the current device (its SM
+ * count decides how far the work is split).  Host-only but for that query;
+ * returns 0 for invalid sizes. */
+size_t q4kv_paged_attention_workspace_size(const srftkv_pages* k, int Hq, const srftkv_paged_batch* batch, int window);
+
 /* Message for the last non-zero return on this host thread ("" if none). */
 const char* srftkv_last_error(void);
 
@@ -281,7 +398,9 @@ const char* srftkv_last_error(void);
  * srftkv_device_fault -- copies the library's device-side fault word for the
  * current device into *fault (0 = none) and clears it.  A kernel whose
  * bounded wait on an asynchronous copy gives up sets a bit here and returns
- * instead of waiting forever.  Synchronises the current device.
+ * instead of waiting forever.  Bits: 0 the codec, 8 the contiguous attention;
+ * paged calls: 16 a slot outside the pool, 17 a block-table entry outside it,
+ * 18 a wait that gave up.  Synchronises the current device.
  */
 int srftkv_device_fault(unsigned int* fault);
 

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "paged.h"
 
 namespace srftkv {
 
@@ -415,7 +416,7 @@ int srftkv_device_fault(unsigned int* fault) {
         set_error("cudaDeviceSynchronize failed");
         return SRFTKV_ERR_CUDA;
     }
-    *fault = codec_take_fault() | (attn_take_fault() << 8);
+    *fault = codec_take_fault() | (attn_take_fault() << 8) | ((paged_codec_take_fault() | paged_attn_take_fault()) << 16);
     return SRFTKV_OK;
 }
 

@@ -1,0 +1,71 @@
+// paged.h -- what the translation units of the paged cache share (the entry
+// points srft_kv_quantize_paged, srft_kv_dequantize_paged and
+// q4kv_paged_attention; layouts and rules in include/srftkv.h).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace srftkv {
+
+// Bits of the paged kernels' fault words (srftkv_device_fault shifts them by 16).
+constexpr unsigned int kFaultSlot = 1u, kFaultPage = 2u, kFaultWait = 4u;
+
+struct PagedSideK {
+    void* x;              // rows [n_tokens][H][d], token stride x_stride elements
+    long long x_stride;
+    uint8_t* codes;
+    uint8_t* scales;
+    const float* lambda;  // [H][d] or null
+    int bits, transform, sfmt;
+};
+
+struct PagedCodecParams {
+    PagedSideK side[2];
+    int n_sides;
+    const int64_t* slots;
+    int n_tokens, H, group, lg_group, lg_page;
+    long long n_slots;    // n_pages * page_size
+    unsigned int* fault;
+    uint32_t sign_mask[128];
+};
+
+// A validated codec call; d and dtype choose the kernel.
+struct PagedCodecCall {
+    PagedCodecParams P;
+    int d, dtype;
+    cudaStream_t stream;
+};
+int paged_quantize(const PagedCodecCall& c);
+int paged_dequantize(const PagedCodecCall& c);
+unsigned int paged_codec_take_fault();
+
+struct PagedAttnParams {
+    const void* q;
+    void* out;
+    long long q_stride, out_stride;
+    const uint8_t *kc, *ks, *vc, *vs;
+    const float *lam_k, *lam_v;
+    const int *table, *seq_lens, *cu_q;
+    int B, max_pages, total_q, max_q, max_len;
+    int Hq, Hkv, rep, n_pages, lg_page, group, lg_group, sfmt;
+    int tr_k, tr_v, window;
+    float qscale;  // sm_scale * log2(e)
+    unsigned int* fault;
+    uint32_t sign_mask[128];
+};
+struct PagedAttnCall {
+    PagedAttnParams P;
+    int d, dtype, bits_k, bits_v;
+    void* workspace;
+    size_t workspace_bytes;
+    cudaStream_t stream;
+};
+size_t paged_attention_workspace(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window);
+int paged_attention(const PagedAttnCall& c);
+unsigned int paged_attn_take_fault();
+
+}  // namespace srftkv
