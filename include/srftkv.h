@@ -377,7 +377,8 @@ typedef struct srftkv_paged_batch {
  * sequence's query count to max_q (rows past it are left as they were).  A
  * block-table entry outside [0, n_pages) reads no memory outside the pools: its
  * tokens count as rows of zeros and bit 17 of the fault word is set.
- * Requires Hq % H == 0, Hq / H <= 128, total_q * Hq < 2^31.
+ * Requires Hq % H == 0, Hq / H <= 128, total_q * Hq < 2^31, max_q * Hq / H <=
+ * 2^22, B * H <= 65535.
  * Values code * scale (lambda times the rotated row) are formed in fp16 where
  * they enter the tensor cores: they must stay below 65504 in size, and those
  * below 2^-14 keep fewer than 11 bits.

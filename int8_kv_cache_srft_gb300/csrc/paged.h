@@ -64,6 +64,20 @@ struct PagedAttnCall {
     size_t workspace_bytes;
     cudaStream_t stream;
 };
+// What a launch of the tile kernel (paged_attn_tile.cuh) adds to the call's parameters
+struct TileWork {
+    int rows_per_block;  // 128 or 256
+    int n_splits;        // ranges of the cache a block is split into
+    int dual;            // both streams hold the same rows (d <= 128)
+    int tps;             // tiles a split
+    int n_parts;         // partial results a row: n_splits * (dual ? 2 : 1); 1: the kernel writes `out` itself
+    int bits_k, bits_v, dtype;
+    float* part_ml;      // [total_q * Hq][n_parts][2]: m (log2 units), l
+    float* part_acc;     // [total_q * Hq][n_parts][D]
+};
+int launch_tile64(const PagedAttnParams& P, const TileWork& W, int blocks, cudaStream_t s);
+int launch_tile128(const PagedAttnParams& P, const TileWork& W, int blocks, cudaStream_t s);
+int launch_tile256(const PagedAttnParams& P, const TileWork& W, int blocks, cudaStream_t s);
 size_t paged_attention_workspace(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window);
 int paged_attention(const PagedAttnCall& c);
 unsigned int paged_attn_take_fault();

@@ -113,6 +113,7 @@ static int check_batch(const char* fn, const srftkv_pages* k, int Hq, const srft
     if ((long long)b->total_q * Hq > INT_MAX) return bad(fn, "total_q * Hq must be below 2^31");
     if (b->max_q > b->total_q) return bad(fn, "max_q must not exceed total_q");
     if (b->B && b->total_q && b->max_q < 1) return bad(fn, "max_q must be at least 1");
+    if ((long long)b->max_q * (Hq / k->H) > (1 << 22)) return bad(fn, "max_q * Hq / H must be at most 2^22");
     if ((long long)b->B * k->H > 65535) return bad(fn, "B * H must be at most 65535");
     return SRFTKV_OK;
 }

@@ -1,14 +1,13 @@
 // paged_attention.cu -- q4kv_paged_attention: causal attention of ragged query
-// rows over a paged packed cache.
+// rows over a paged packed cache: how a call's work is divided, and the kernel
+// that joins partial results.
 //
 // In the rotated coordinates of the cache (R orthogonal): q~ = R q / lambda_K *
 // sm_scale * log2 e, s_t = q~ . (codes_K scale_K)_t, an online softmax over the
 // visible tokens, o = sum_t p_t (codes_V scale_V)_t / sum_t p_t, and
 // out = R^T (o / lambda_V).
-//
-// One warp a (query token, head): it walks the sequence's tokens, each lane
-// holding d/32 coordinates.
-#include "codec_impl.cuh"
+#include <algorithm>
+
 #include "paged.h"
 #include "paged_rotate.cuh"
 
@@ -16,9 +15,13 @@ namespace srftkv {
 
 static __device__ unsigned int g_paged_attn_fault;
 
+// Join the partial results of one (query token, head), one warp a row:
+// o = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p, then / lambda_V and R^T.
+// Partials with m = -inf are empty and their acc is not read.
 template <int D, typename T>
-__global__ void __launch_bounds__(128) paged_attn_warp_kernel(const __grid_constant__ PagedAttnParams P, int bits_k,
-                                                              int bits_v) {
+__global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_constant__ PagedAttnParams P, int n_parts,
+                                                                 const float* __restrict__ part_ml,
+                                                                 const float* __restrict__ part_acc) {
     constexpr int E = D / 32;
     __shared__ float2 sm[4][D / 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -28,70 +31,89 @@ __global__ void __launch_bounds__(128) paged_attn_warp_kernel(const __grid_const
     const int q0 = P.cu_q ? P.cu_q[b] : b;
     const int m = min(P.cu_q ? P.cu_q[b + 1] - q0 : 1, P.max_q);
     if (i >= m || q0 < 0 || q0 + i >= P.total_q) return;
-    const int len = min(max(P.seq_lens[b], 0), P.max_len);
-    const int pos = len - m + i;
-    float v[E], l[E];
-    rot::load_row<D, T>(static_cast<const T*>(P.q) + (q0 + i) * P.q_stride + (long long)hq * D, lane, v);
-    rot::forward<D>(v, lane, P.tr_k, P.sign_mask, sm[warp]);
-    if (P.lam_k) {
-        rot::load_lambda<D>(P.lam_k + (long long)h * D, lane, l);
+    const long long at = ((long long)(q0 + i) * P.Hq + hq) * n_parts;
+    float M = -INFINITY;
+    for (int p = lane; p < n_parts; p += 32) M = fmaxf(M, part_ml[2 * (at + p)]);
 #pragma unroll
-        for (int j = 0; j < E; ++j) v[j] = __fdiv_rn(v[j], l[j]);
-    }
-    float o[E] = {}, mx = -INFINITY, den = 0.f;
-    const int ng = D >> P.lg_group, gi = (E * lane) >> P.lg_group;
-    const int sb = P.sfmt == SRFTKV_SCALE_FP32 ? 4 : P.sfmt == SRFTKV_SCALE_FP16 ? 2 : 1;
-    for (int t = P.window ? max(0, pos - P.window + 1) : 0; t <= pos; ++t) {
-        const int pg = P.table[(long long)b * P.max_pages + (t >> P.lg_page)];
-        const bool ok = (unsigned)pg < (unsigned)P.n_pages;
-        if (!ok && lane == 0) atomicOr(P.fault, kFaultPage);
-        const long long row = (((long long)pg * P.Hkv + h) << P.lg_page) | (t & ((1 << P.lg_page) - 1));
-        float c[E], s = 0.f;
-        if (ok) {
-            if (bits_k == 4) rot::load_codes<D, 4>(P.kc + row * (D / 2), lane, c);
-            else rot::load_codes<D, 8>(P.kc + row * D, lane, c);
-            const float sc = load_scale(P.ks + row * ng * sb, gi, P.sfmt);
+    for (int k = 16; k; k >>= 1) M = fmaxf(M, rot::sx(M, k));
+    float o[E] = {}, l = 0.f;
+    if (M != -INFINITY) {
+#pragma unroll 4
+        for (int p = 0; p < n_parts; ++p) {
+            const float2 ml = *reinterpret_cast<const float2*>(part_ml + 2 * (at + p));
+            if (ml.x == -INFINITY) continue;
+            const float w = exp2f(ml.x - M);
+            l = fmaf(w, ml.y, l);
+            float a[E];
+            rot::load_lambda<D>(part_acc + (at + p) * D, lane, a);
 #pragma unroll
-            for (int j = 0; j < E; ++j) s = fmaf(c[j] * sc, v[j], s);
+            for (int j = 0; j < E; ++j) o[j] = fmaf(w, a[j], o[j]);
         }
-#pragma unroll
-        for (int k = 16; k; k >>= 1) s += rot::sx(s, k);
-        s *= P.qscale;
-        const float mn = fmaxf(mx, s), f = exp2f(mx - mn), p = exp2f(s - mn);
-        mx = mn;
-        den = den * f + p;
-        float sc = 0.f;
-        if (ok) {
-            if (bits_v == 4) rot::load_codes<D, 4>(P.vc + row * (D / 2), lane, c);
-            else rot::load_codes<D, 8>(P.vc + row * D, lane, c);
-            sc = load_scale(P.vs + row * ng * sb, gi, P.sfmt);
-        }
-#pragma unroll
-        for (int j = 0; j < E; ++j) o[j] = ok ? fmaf(p * sc, c[j], o[j] * f) : o[j] * f;
     }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int j = 0; j < E; ++j) o[j] *= inv;
     if (P.lam_v) {
-        rot::load_lambda<D>(P.lam_v + (long long)h * D, lane, l);
+        float lam[E];
+        rot::load_lambda<D>(P.lam_v + (long long)h * D, lane, lam);
 #pragma unroll
-        for (int j = 0; j < E; ++j) o[j] = __fdiv_rn(o[j], l[j]);
+        for (int j = 0; j < E; ++j) o[j] = __fdiv_rn(o[j], lam[j]);
     }
     rot::inverse<D>(o, lane, P.tr_v, P.sign_mask, sm[warp]);
     rot::store_row<D, T>(static_cast<T*>(P.out) + (q0 + i) * P.out_stride + (long long)hq * D, lane, o);
 }
 
+// How a call is divided: a pure function of its sizes (the workspace size and the launch both ask for it).
+struct Plan {
+    TileWork W;
+    int blocks;      // row blocks a (sequence, kv head)
+    size_t acc_off;  // part_ml at 0, part_acc here
+    size_t bytes;
+};
+static Plan make_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window) {
+    Plan p = {};
+    const int rep = Hq / Hkv, bn = d == 256 ? 64 : 128;
+    const long long rows = (long long)max_q * rep;
+    p.W.dual = d != 256 && rows <= 128;
+    p.W.rows_per_block = d == 256 || p.W.dual ? 128 : 256;
+    p.blocks = (int)((rows + p.W.rows_per_block - 1) / p.W.rows_per_block);
+    // the most tiles any block sees
+    long long see = max_len;
+    if (window) see = std::min<long long>(see, (long long)window + (p.W.rows_per_block - 1) / rep + 1);
+    long long tiles = (see + bn - 1) / bn;
+    if (window) tiles = std::min<long long>((max_len + bn - 1) / bn, tiles + 1);
+    // one CTA runs on an SM: split the cache where that shortens waves * (tiles a split + the fixed part)
+    const long long base = (long long)B * Hkv * p.blocks, sms = device_sm_count(), fixed = 6;
+    long long best = 1, best_cost = -1;
+    for (long long s = 1; s <= std::min<long long>(tiles, 64); ++s) {
+        const long long tps = (tiles + s - 1) / s;
+        if (s > 1 && (tiles + tps - 1) / tps != s) continue;
+        const long long cost = (base * s + sms - 1) / sms * (tps + fixed);
+        if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
+    }
+    p.W.n_splits = (int)best;
+    p.W.tps = (int)((tiles + best - 1) / best);
+    p.W.n_parts = p.W.n_splits * (p.W.dual ? 2 : 1);
+    if (p.W.n_parts > 1) {
+        const size_t n = (size_t)total_q * Hq * p.W.n_parts;
+        p.acc_off = (n * 8 + 255) / 256 * 256;
+        p.bytes = p.acc_off + n * d * 4;
+    }
+    return p;
+}
+
 size_t paged_attention_workspace(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window) {
-    return 16;
+    if (B == 0 || total_q == 0) return 0;
+    return make_plan(d, Hq, Hkv, B, total_q, max_q, max_len, window).bytes;
 }
 
 template <int D>
-static void launch(const PagedAttnCall& c, const PagedAttnParams& P) {
+static void launch_combine(const PagedAttnCall& c, const PagedAttnParams& P, const TileWork& W) {
     const dim3 grid((unsigned)(((long long)P.max_q * P.Hq + 3) / 4), P.B);
     if (c.dtype == SRFTKV_DTYPE_BF16)
-        paged_attn_warp_kernel<D, __nv_bfloat16><<<grid, 128, 0, c.stream>>>(P, c.bits_k, c.bits_v);
+        paged_attn_combine_kernel<D, __nv_bfloat16><<<grid, 128, 0, c.stream>>>(P, W.n_parts, W.part_ml, W.part_acc);
     else
-        paged_attn_warp_kernel<D, __half><<<grid, 128, 0, c.stream>>>(P, c.bits_k, c.bits_v);
+        paged_attn_combine_kernel<D, __half><<<grid, 128, 0, c.stream>>>(P, W.n_parts, W.part_ml, W.part_acc);
 }
 
 int paged_attention(const PagedAttnCall& c) {
@@ -100,13 +122,26 @@ int paged_attention(const PagedAttnCall& c) {
     void* f = nullptr;
     if (symbol_address(cache, &g_paged_attn_fault, &f, "the paged attention's fault word")) return SRFTKV_ERR_CUDA;
     P.fault = static_cast<unsigned int*>(f);
-    if (c.d == 64) launch<64>(c, P);
-    else if (c.d == 128) launch<128>(c, P);
-    else launch<256>(c, P);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) {
-        set_error("paged attention launch failed: %s", cudaGetErrorString(e));
-        return SRFTKV_ERR_CUDA;
+    Plan plan = make_plan(c.d, P.Hq, P.Hkv, P.B, P.total_q, P.max_q, P.max_len, P.window);
+    TileWork& W = plan.W;
+    W.bits_k = c.bits_k;
+    W.bits_v = c.bits_v;
+    W.dtype = c.dtype;
+    W.part_ml = static_cast<float*>(c.workspace);
+    W.part_acc = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + plan.acc_off);
+    const int rc = c.d == 64    ? launch_tile64(P, W, plan.blocks, c.stream)
+                   : c.d == 128 ? launch_tile128(P, W, plan.blocks, c.stream)
+                                : launch_tile256(P, W, plan.blocks, c.stream);
+    if (rc) return rc;
+    if (W.n_parts > 1) {
+        if (c.d == 64) launch_combine<64>(c, P, W);
+        else if (c.d == 128) launch_combine<128>(c, P, W);
+        else launch_combine<256>(c, P, W);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) {
+            set_error("paged attention launch failed: %s", cudaGetErrorString(e));
+            return SRFTKV_ERR_CUDA;
+        }
     }
     return SRFTKV_OK;
 }

@@ -1,0 +1,771 @@
+// paged_attn_tile.cuh -- attention of blocks of query rows over the paged
+// cache on the 5th-generation tensor cores (each d in its own translation
+// unit).  The query rows of one sequence and kv head are its query tokens
+// times the Hq / H heads that read that kv head, token-major; a CTA takes 256
+// (d = 64, 128) or 128 (d = 256) of them and a range of the cache in tiles of
+// BN tokens.
+//
+//   q~ = R_s q * sm_scale log2(e) / lambda_K      (one contraction, R_s as fp16 hi + lo)
+//   S  = q~ . K^T,  K = code * scale in fp16       (M = 128 rows, N = BN tokens)
+//   P  = 2^(S - m), online maximum m and sum l in fp32, one thread a row
+//   O += P . V, V = code * scale in fp16           (P from tensor memory)
+//   out = R_s^T (O / l / lambda_V)                 (one contraction more)
+//
+// The cache is never rotated back token by token: R_s is orthogonal, so the
+// scores and the sum are the same in its coordinates.
+//
+// Warps: 0-7 softmax (a group of four a q tile; warp w reads tensor-memory
+// lanes 32(w%4)..+31), 8-15 dequantise tiles from the pages into shared memory
+// (128-byte-swizzled rows, two stages of K and of V), 16 issues the MMAs.  The
+// two q tiles alternate on the tensor cores: while one is in its softmax the
+// other's P.V and next S run.  At d = 256 O takes half of tensor memory, so
+// one q tile alternates between two S buffers instead.
+//
+// Few rows (at most 128 a sequence and kv head, "dual"): both streams hold the
+// same rows and take every other tile, each with its own m, l and O, joined by
+// the combine kernel like splits of the cache.
+//
+// Roundings: q~, K, V, P to fp16 (2^-11 each; K and V are exact code * scale
+// products rounded once; with fp32 scales the scale enters as hi + lo), and
+// O / l and R_s to fp16 on the way out.  m, l, S and O are fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "codec_tc_common.cuh"
+#include "paged.h"
+#include "ptx.cuh"
+#include "srft_math.cuh"
+#include "tcgen05.cuh"
+
+namespace srftkv {
+
+namespace tile {
+
+constexpr int SM_WARPS = 8, DQ_WARPS = 8;
+constexpr int THREADS = (SM_WARPS + DQ_WARPS + 1) * 32;
+constexpr float kLazy = 8.f;  // O is rescaled when the maximum grew by more than this (P stays below 2^8)
+
+template <int D>
+struct Cfg {
+    static constexpr int NQ = D == 256 ? 1 : 2;    // q tiles of 128 rows
+    static constexpr int BN = D == 256 ? 64 : 128; // tokens a tile
+    static constexpr int QB = 128 * D * 2;         // bytes of a q tile
+    static constexpr int TB = BN * D * 2;          // bytes of a K or V tile
+    static constexpr int OFF_K = NQ * QB;
+    static constexpr int OFF_V = OFF_K + 2 * TB;
+    static constexpr int OFF_TW = OFF_V + 2 * TB;       // cos, -sin of 2 pi m / d
+    static constexpr int OFF_SG = OFF_TW + D * 8;       // sign words
+    static constexpr int OFF_BAR = OFF_SG + D * 2;
+    static constexpr int USED = OFF_BAR + 256;
+    // one CTA an SM: it owns all of tensor memory
+    static constexpr int SMEM = (USED > 120 * 1024 ? USED : 120 * 1024) + 1024;
+    static constexpr int O_COL = 256;
+    static constexpr int S_STEP = NQ == 2 ? 128 : BN;   // columns between S buffers
+    static constexpr int R_COL = NQ == 2 ? 0 : O_COL;   // rotated q (fp32) before the loop
+    // P.  At d = 128 tensor memory is full and P takes the columns its S was read from: the next S into them is
+    // issued after the P.V that reads them and has its shape, so the two run in order.  At the other d the two
+    // shapes differ (their order is not given) and there are columns to spare; a P is then only overwritten after
+    // the next S of its buffer was seen complete, whose commit covers the P.V before it.
+    static constexpr int P_COL = D == 128 ? 0 : D == 64 ? 384 : 128;
+    static constexpr int P_STEP = D == 128 ? S_STEP : BN / 2;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+// B operand stored MN-major (rows of the contraction index, 64 of N a 128-byte row): 8-row groups 1024 bytes
+// apart, 64-column blocks `lbo` bytes apart, 128-byte swizzle
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(lbo >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
+    return tc::idesc_f16_f32(M, N) | (b_mn ? 1u << 16 : 0u);
+}
+
+__device__ __forceinline__ float ex2(float x) {  // 2^x, relative error about 2^-22
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16-byte chunk (8 consecutive inputs x0..) of row n of R_s as fp16 hi (and lo)
+template <int D, bool LO>
+__device__ __forceinline__ void r_chunk(int n, int x0, bool srht, const float2* tw, const uint32_t* sg, uint4& hi,
+                                        uint4& lo) {
+    const float isd = rsqrtf((float)D), c2 = 1.41421356237309505f * isd;
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int x = x0 + 2 * j + e;
+            if (srht) v[e] = (__popc(n & x) & 1) ? -isd : isd;
+            else if (n == 0) v[e] = isd;
+            else if (n == 1) v[e] = (x & 1) ? -isd : isd;
+            else {
+                const float2 w = tw[((n >> 1) * x) & (D - 1)];
+                v[e] = c2 * ((n & 1) ? w.y : w.x);
+            }
+            if (sg[x >> 1] & (e ? 0x80000000u : 0x8000u)) v[e] = -v[e];
+        }
+        if constexpr (LO) split_pair_h2(v[0], v[1], h[j], l[j]);
+        else h[j] = pack_half2(v[0], v[1]);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    if constexpr (LO) lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// eight 4-bit codes of word w (or eight 8-bit codes of words w, w2) times the scale, as fp16 pairs in the
+// order of dq_kperm; LO: the scale is sh + sl
+template <int BITS, bool LO>
+__device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t w2, uint32_t sh, uint32_t sl) {
+    uint32_t c[4];
+    if constexpr (BITS == 4) {
+        const uint32_t ws = w >> 8;
+        c[0] = codes_lo4(w);
+        c[1] = codes_hi4(w);
+        c[2] = codes_lo4(ws);
+        c[3] = codes_hi4(ws);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            c[j] = codes_b8(__byte_perm(w, w2, j | (j << 4) | ((4 + j) << 8) | ((4 + j) << 12)));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = LO ? h2fma(c[j], sh, h2mul(c[j], sl)) : h2mul(c[j], sh);
+    return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// The raw bytes of one dequantising thread's piece of a tile row: DP coordinates (32 or 64)
+template <int DP>
+struct Piece {
+    uint32_t w[DP / 4];   // 8-bit: DP/4 words, 4-bit: the first DP/8
+    float sc[DP / 16];    // scale of each 16-coordinate unit
+};
+
+// Load the piece of row `row` (packed row index, -1: zeros) that starts at coordinate x0
+template <int D, int DP>
+__device__ __forceinline__ void load_piece(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                           long long row, int x0, int bits, int sfmt, int lg_group, Piece<DP>& p) {
+    constexpr int U = DP / 16;
+    if (row < 0) {
+#pragma unroll
+        for (int i = 0; i < DP / 4; ++i) p.w[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < U; ++i) p.sc[i] = 0.f;
+        return;
+    }
+    if (bits == 4) {
+        const uint4* c = reinterpret_cast<const uint4*>(codes + row * (D / 2) + x0 / 2);
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) {
+            const uint4 v = __ldg(c + i);
+            p.w[4 * i] = v.x, p.w[4 * i + 1] = v.y, p.w[4 * i + 2] = v.z, p.w[4 * i + 3] = v.w;
+        }
+    } else {
+        const uint4* c = reinterpret_cast<const uint4*>(codes + row * D + x0);
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+            const uint4 v = __ldg(c + i);
+            p.w[4 * i] = v.x, p.w[4 * i + 1] = v.y, p.w[4 * i + 2] = v.z, p.w[4 * i + 3] = v.w;
+        }
+    }
+    const int ng = D >> lg_group;
+    if (lg_group == 4) {  // one scale a unit: a vector of them
+        if (sfmt == SRFTKV_SCALE_FP32) {
+            const float* s = reinterpret_cast<const float*>(scales) + row * ng + x0 / 16;
+            if constexpr (U == 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(s));
+                p.sc[0] = v.x, p.sc[1] = v.y, p.sc[2] = v.z, p.sc[3] = v.w;
+            } else {
+                const float2 v = __ldg(reinterpret_cast<const float2*>(s));
+                p.sc[0] = v.x, p.sc[1] = v.y;
+            }
+        } else if (sfmt == SRFTKV_SCALE_FP16) {
+            const __half* s = reinterpret_cast<const __half*>(scales) + row * ng + x0 / 16;
+            uint32_t v[U / 2];
+            if constexpr (U == 4) {
+                const uint2 t = __ldg(reinterpret_cast<const uint2*>(s));
+                v[0] = t.x, v[1] = t.y;
+            } else {
+                v[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+            }
+#pragma unroll
+            for (int i = 0; i < U / 2; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
+                p.sc[2 * i] = f.x, p.sc[2 * i + 1] = f.y;
+            }
+        } else {
+            uint32_t v;
+            if constexpr (U == 4) v = __ldg(reinterpret_cast<const uint32_t*>(scales + row * ng + x0 / 16));
+            else v = __ldg(reinterpret_cast<const unsigned short*>(scales + row * ng + x0 / 16));
+#pragma unroll
+            for (int i = 0; i < U; ++i) p.sc[i] = __uint_as_float(((v >> (8 * i)) & 0xFFu) << 23);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const long long at = row * ng + ((x0 + 16 * i) >> lg_group);
+            if (sfmt == SRFTKV_SCALE_FP32) p.sc[i] = __ldg(reinterpret_cast<const float*>(scales) + at);
+            else if (sfmt == SRFTKV_SCALE_FP16) p.sc[i] = __half2float(__ldg(reinterpret_cast<const __half*>(scales) + at));
+            else p.sc[i] = __uint_as_float((uint32_t)__ldg(scales + at) << 23);
+        }
+    }
+}
+
+// Write a piece as fp16 into row r of a swizzled tile of BN rows
+template <int D, int BN, int DP, int BITS, bool LO>
+__device__ __forceinline__ void store_piece(uint8_t* tile, int r, int x0, const Piece<DP>& p) {
+#pragma unroll
+    for (int u = 0; u < DP / 16; ++u) {
+        const __half h = __float2half_rn(p.sc[u]);
+        const uint32_t sh = half2_bcast(h);
+        const uint32_t sl = LO ? half2_bcast(__float2half_rn(p.sc[u] - __half2float(h))) : 0u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int k = 2 * u + e;  // 8-coordinate chunk of the piece
+            const uint4 v = BITS == 4 ? dequant8<4, LO>(p.w[k], 0u, sh, sl)
+                                      : dequant8<8, LO>(p.w[(2 * k) % (DP / 4)], p.w[(2 * k + 1) % (DP / 4)], sh, sl);
+            const int x = x0 + 8 * k;
+            *reinterpret_cast<uint4*>(tile + (x >> 6) * (BN * 128) + r * 128 + ((((x & 63) >> 3) ^ (r & 7)) << 4)) = v;
+        }
+    }
+}
+template <int D, int BN, int DP>
+__device__ __forceinline__ void store_piece_any(uint8_t* tile, int r, int x0, int bits, bool lo, const Piece<DP>& p) {
+    if (bits == 4) {
+        if (lo) store_piece<D, BN, DP, 4, true>(tile, r, x0, p);
+        else store_piece<D, BN, DP, 4, false>(tile, r, x0, p);
+    } else {
+        if (lo) store_piece<D, BN, DP, 8, true>(tile, r, x0, p);
+        else store_piece<D, BN, DP, 8, false>(tile, r, x0, p);
+    }
+}
+
+}  // namespace tile
+
+template <int D>
+__global__ void __launch_bounds__(tile::THREADS, 1)
+    paged_attn_tile_kernel(const __grid_constant__ PagedAttnParams P, const __grid_constant__ TileWork W) {
+    using C = tile::Cfg<D>;
+    constexpr int NQ = C::NQ, BN = C::BN;
+    constexpr int SMW = 4 * NQ;  // softmax warps at work
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+
+    // ---- this CTA's rows and tiles ----
+    const int b = blockIdx.x / P.Hkv, h = blockIdx.x - b * P.Hkv;
+    const int blk = gridDim.y - 1 - blockIdx.y;  // the longest rows (causal) first
+    const int split = blockIdx.z;
+    const int q0 = P.cu_q ? P.cu_q[b] : b;
+    int m_tok = min(P.cu_q ? P.cu_q[b + 1] - q0 : 1, P.max_q);
+    if (q0 < 0) m_tok = 0;
+    m_tok = min(m_tok, P.total_q - q0);
+    const int n_rows = m_tok * P.rep;
+    const int row0 = blk * W.rows_per_block;
+    if (row0 >= n_rows) return;
+    const int len = min(max(P.seq_lens[b], 0), P.max_len);
+    const int rows_here = min(W.rows_per_block, n_rows - row0);
+    const int pos_lo = len - m_tok + row0 / P.rep, pos_hi = len - m_tok + (row0 + rows_here - 1) / P.rep;
+    int ta = P.window ? max(0, pos_lo - P.window + 1) / BN : 0;
+    int tb = pos_hi >= 0 ? pos_hi / BN + 1 : 0;
+    ta = ta + split * W.tps;
+    tb = min(tb, W.n_splits > 1 ? ta + W.tps : tb);
+    const int n = max(0, tb - ta);  // tiles
+    const bool dual = NQ == 2 && W.dual;
+
+    // row r of the block -> its row of q / out
+    auto out_row = [&](int r, int& i, int& hq) {
+        i = (row0 + r) / P.rep;
+        hq = h * P.rep + (row0 + r - i * P.rep);
+        i += q0;
+    };
+    if (n == 0) {  // nothing visible: zeros, or empty partials
+        for (int r = threadIdx.x; r < rows_here; r += blockDim.x) {
+            int i, hq;
+            out_row(r, i, hq);
+            if (W.n_parts == 1) {
+                uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + i * P.out_stride + (long long)hq * D);
+                for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
+            } else {
+                const int per = W.n_parts / W.n_splits;
+                for (int e = 0; e < per; ++e) {
+                    float* ml = W.part_ml + (((long long)i * P.Hq + hq) * W.n_parts + split * per + e) * 2;
+                    ml[0] = -INFINITY;
+                    ml[1] = 0.f;
+                }
+            }
+        }
+        return;
+    }
+
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    auto bar = [&](int i) { return ptx::smem_u32(&bars[i]); };
+    constexpr int K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, P_FULL = 10, PV_DONE = 12, ROT = 14,
+                  R_FULL = 15, EP_FULL = 16, OUT_FULL = 17, N_BARS = 18;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&bars[N_BARS]);
+    float2* tw = reinterpret_cast<float2*>(smem + C::OFF_TW);
+    uint32_t* sg = reinterpret_cast<uint32_t*>(smem + C::OFF_SG);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(bar(K_FULL + s), tile::DQ_WARPS);
+            ptx::mbar_init(bar(V_FULL + s), tile::DQ_WARPS);
+            ptx::mbar_init(bar(K_EMPTY + s), 1);
+            ptx::mbar_init(bar(V_EMPTY + s), 1);
+            ptx::mbar_init(bar(S_FULL + s), 1);
+            ptx::mbar_init(bar(P_FULL + s), 4);
+            ptx::mbar_init(bar(PV_DONE + s), 1);
+        }
+        ptx::mbar_init(bar(ROT), 1);
+        ptx::mbar_init(bar(R_FULL), tile::DQ_WARPS);
+        ptx::mbar_init(bar(EP_FULL), SMW);
+        ptx::mbar_init(bar(OUT_FULL), 1);
+        ptx::fence_barrier_init();
+    }
+    if (warp == 16) {
+        tc::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+        tc::tmem_relinquish();
+    }
+    for (int m = threadIdx.x; m < D; m += blockDim.x) tw[m] = make_float2(tw_re_lane(m * (256 / D)), tw_im_lane(m * (256 / D)));
+    for (int i = threadIdx.x; i < D / 2; i += blockDim.x) sg[i] = P.sign_mask[i];
+
+    // ---- q rows as fp16 into the q tiles (zeros past the last row) ----
+    const int q_rows = dual || NQ == 1 ? 128 : 256;
+    for (int c = threadIdx.x; c < q_rows * (D / 8); c += blockDim.x) {
+        const int r = c / (D / 8), ch = c % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < rows_here) {
+            int i, hq;
+            out_row(r, i, hq);
+            v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + i * P.q_stride + (long long)hq * D) + ch);
+            if (W.dtype == SRFTKV_DTYPE_BF16) {  // 8 significant bits: exact in fp16 within its range
+                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xFFFF0000u);
+                    w[j] = pack_half2(lo, hi);
+                }
+            }
+        }
+        *reinterpret_cast<uint4*>(smem + (r >> 7) * C::QB + (ch >> 3) * 16384 + (r & 127) * 128 +
+                                  (((ch & 7) ^ (r & 7)) << 4)) = v;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    bool failed = false;
+
+    // ---- rotate them: R_s rows in steps of 128 outputs, hi and lo, in the K and V stages ----
+    const int n_qt = q_rows / 128;
+    constexpr int NB = D < 128 ? D : 128;
+    for (int nh = 0; nh < D / NB; ++nh) {
+        for (int c = threadIdx.x; c < NB * (D / 8); c += blockDim.x) {
+            const int nr = c / (D / 8), ch = c % (D / 8);
+            uint4 hi, lo;
+            tile::r_chunk<D, true>(nh * NB + nr, 8 * ch, P.tr_k == SRFTKV_TRANSFORM_SRHT, tw, sg, hi, lo);
+            uint8_t* at = smem + C::OFF_K + (ch >> 3) * (NB * 128) + nr * 128 + (((ch & 7) ^ (nr & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) = hi;
+            *reinterpret_cast<uint4*>(at + NB * D * 2) = lo;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < n_qt; ++i)
+#pragma unroll 1
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint64_t ad = tc::sw128_desc(sbase + i * C::QB + (ks >> 2) * 16384 + (ks & 3) * 32);
+                    const uint32_t bo = sbase + C::OFF_K + (ks >> 2) * (NB * 128) + (ks & 3) * 32;
+                    const uint32_t dst = tmem + C::R_COL + i * 128 + nh * NB;
+                    tc::mma_f16(dst, ad, tc::sw128_desc(bo), tile::idesc(128, NB, false), ks > 0);
+                    tc::mma_f16(dst, ad, tc::sw128_desc(bo + NB * D * 2), tile::idesc(128, NB, false), 1);
+                }
+            tc::commit(bar(ROT));
+        }
+        if (!ptx::mbar_wait_bounded(bar(ROT), nh & 1)) failed = true;
+        tc::fence_after_sync();
+        __syncthreads();
+    }
+    // each softmax thread scales its row and writes it back as the A operand, in the order of dq_kperm
+    if (warp < 4 * n_qt && !failed) {
+        const int i = warp >> 2, r = 32 * (warp & 3) + lane;
+        uint8_t* qrow = smem + i * C::QB + r * 128;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tc::ld_32x32b_x32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C::R_COL + i * 128 + 32 * c, v);
+            tc::wait_ld(v);
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]) * P.qscale;
+            if (P.lam_k) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) f[j] = __fdiv_rn(f[j], __ldg(P.lam_k + (long long)h * D + 32 * c + j));
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int ch = 4 * c + w;
+                *reinterpret_cast<uint4*>(qrow + (ch >> 3) * 16384 + (((ch & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(pack_half2(f[8 * w], f[8 * w + 4]), pack_half2(f[8 * w + 1], f[8 * w + 5]),
+                               pack_half2(f[8 * w + 2], f[8 * w + 6]), pack_half2(f[8 * w + 3], f[8 * w + 7]));
+            }
+        }
+        ptx::fence_proxy_async_smem();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+
+    const int n0 = dual ? (n + 1) / 2 : n;  // steps of stream 0
+    auto steps_of = [&](int i) { return dual ? (n + 1 - i) / 2 : n; };
+    auto wait1 = [&](int which, uint32_t parity) -> bool {  // one thread
+        if (ptx::mbar_wait_bounded(bar(which), parity)) return true;
+        failed = true;
+        return false;
+    };
+    auto wait = [&](int which, uint32_t parity) -> bool {  // a whole warp, converged afterwards
+        if (__all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar(which), parity))) return true;
+        failed = true;
+        return false;
+    };
+
+    if (!failed && warp >= SMW && warp < 8) {
+        // (d = 256: the second softmax group has nothing to do)
+    } else if (!failed && warp < SMW) {
+        // =========================== softmax ===========================
+        const int i = warp >> 2;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const int r = (dual ? 0 : i * 128) + 32 * (warp & 3) + lane;
+        const bool live = r < rows_here;
+        const bool any_live = __any_sync(0xffffffffu, live);
+        int oi = 0, hq = 0;
+        if (live) out_row(r, oi, hq);
+        const int pos = live ? len - m_tok + (row0 + r) / P.rep : -1;
+        const int first = P.window ? pos - P.window + 1 : 0;
+        const uint32_t o_col = tmem + lanes + C::O_COL + (NQ == 2 ? i * D : 0);
+        float mx = -INFINITY, l = 0.f;
+        const int steps = steps_of(i);
+        for (int j = 0; j < steps; ++j) {
+            const int sb = NQ == 2 ? i : (j & 1);
+            if (!wait(S_FULL + sb, NQ == 2 ? (j & 1) : ((j >> 1) & 1))) break;
+            if (any_live) {
+                tc::fence_after_sync();
+                const int t0 = (ta + (dual ? 2 * j + i : j)) * BN;
+                const uint32_t s_col = tmem + lanes + sb * C::S_STEP, p_col = tmem + lanes + C::P_COL + sb * C::P_STEP;
+                const int hi = pos - t0, lo = first - t0;  // visible columns lo .. hi
+                const bool full = __all_sync(0xffffffffu, hi >= BN - 1 && lo <= 0);
+                float mt = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < BN / 32; ++c) {
+                    uint32_t v[32];
+                    tc::ld_32x32b_x32(s_col + 32 * c, v);
+                    tc::wait_ld(v);
+                    if (!full) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e > hi || 32 * c + e < lo) v[e] = 0xFF800000u;
+                    }
+                    float a[4] = {mt, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) a[e & 3] = fmaxf(a[e & 3], __uint_as_float(v[e]));
+                    mt = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+                }
+                // the maximum in use may lag behind the true one by kLazy
+                const bool grow = mt > mx + tile::kLazy || (mx == -INFINITY && mt > -INFINITY);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float mn = fmaxf(mx, mt);
+                    const float f = mx == -INFINITY ? 0.f : tile::ex2(mx - mn);  // (O is 0 or unset while mx is -inf)
+                    l *= f;
+                    mx = mn;
+                    if (j > 0) {
+                        if (!wait(PV_DONE + (NQ == 2 ? i : 0), (j - 1) & 1)) break;
+                        tc::fence_after_sync();
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t v[32];
+                            tc::ld_32x32b_x32(o_col + 32 * c, v);
+                            tc::wait_ld(v);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                            tc::st_32x32b_x32(o_col + 32 * c, v);
+                        }
+                    }
+                }
+                const float mu = mx == -INFINITY ? 0.f : mx;
+                float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int c = 0; c < BN / 32; ++c) {
+                    uint32_t v[32], p[16];
+                    tc::ld_32x32b_x32(s_col + 32 * c, v);
+                    tc::wait_ld(v);
+                    if (!full) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e > hi || 32 * c + e < lo) v[e] = 0xFF800000u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float a = tile::ex2(__uint_as_float(v[2 * e]) - mu);
+                        const float d = tile::ex2(__uint_as_float(v[2 * e + 1]) - mu);
+                        s4[(2 * e) & 3] += a;
+                        s4[(2 * e + 1) & 3] += d;
+                        p[e] = pack_half2(a, d);
+                    }
+                    tc::st_32x32b_x16(p_col + 16 * c, p);
+                }
+                l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                tc::wait_st();
+                tc::fence_before_sync();
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(P_FULL + sb));
+        }
+        // ---- the end: O / l rotated back, or a partial result ----
+        if (!failed && steps > 0) {
+            // one q tile: the last S was issued before the P.V of the step before it, so that phase has to be seen
+            // first (a parity tells two phases apart, not three)
+            if (NQ == 1 && steps > 1) wait(PV_DONE, (steps - 2) & 1);
+            if (!failed && wait(PV_DONE + (NQ == 2 ? i : 0), (steps - 1) & 1)) tc::fence_after_sync();
+        }
+        if (W.n_parts > 1) {
+            if (!failed && live) {
+                const int part = dual ? 2 * split + i : split;
+                const long long at = ((long long)oi * P.Hq + hq) * W.n_parts + part;
+                W.part_ml[2 * at] = steps ? mx : -INFINITY;
+                W.part_ml[2 * at + 1] = l;
+            }
+            if (!failed && steps > 0 && any_live) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tc::ld_32x32b_x32(o_col + 32 * c, v);
+                    tc::wait_ld(v);
+                    if (live) {
+                        const int part = dual ? 2 * split + i : split;
+                        uint4* o = reinterpret_cast<uint4*>(W.part_acc + (((long long)oi * P.Hq + hq) * W.n_parts + part) * D + 32 * c);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {  // column 8w + 2k + e holds coordinate 8w + k + 4e
+                            o[2 * w] = make_uint4(v[8 * w], v[8 * w + 2], v[8 * w + 4], v[8 * w + 6]);
+                            o[2 * w + 1] = make_uint4(v[8 * w + 1], v[8 * w + 3], v[8 * w + 5], v[8 * w + 7]);
+                        }
+                    }
+                }
+            }
+        } else if (!failed) {
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            uint8_t* arow = smem + i * C::QB + (32 * (warp & 3) + lane) * 128;
+            const int rr = 32 * (warp & 3) + lane;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                tc::ld_32x32b_x32(o_col + 32 * c, v);
+                tc::wait_ld(v);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    float f[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)  // natural coordinate k from column 2 (k % 4) + k / 4
+                        f[k] = l > 0.f ? __uint_as_float(v[8 * w + 2 * (k & 3) + (k >> 2)]) * inv : 0.f;
+                    if (P.lam_v) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            f[k] = __fdiv_rn(f[k], __ldg(P.lam_v + (long long)h * D + 32 * c + 8 * w + k));
+                    }
+                    const int ch = 4 * c + w;
+                    *reinterpret_cast<uint4*>(arow + (ch >> 3) * 16384 + (((ch & 7) ^ (rr & 7)) << 4)) =
+                        make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]),
+                                   pack_half2(f[6], f[7]));
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(EP_FULL));
+            if (wait(OUT_FULL, 0) && any_live) {
+                tc::fence_after_sync();
+                uint16_t* o = static_cast<uint16_t*>(P.out) + oi * P.out_stride + (long long)hq * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tc::ld_32x32b_x32(tmem + lanes + i * 128 + 32 * c, v);
+                    tc::wait_ld(v);
+                    uint32_t w[16];
+                    if (W.dtype == SRFTKV_DTYPE_BF16) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                            w[e] = *reinterpret_cast<const uint32_t*>(&t);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = pack_half2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                    }
+                    if (live) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4*>(o + 32 * c)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    }
+                }
+            }
+        }
+    } else if (!failed && warp < 16) {
+        // =========================== dequantise ===========================
+        constexpr int DP = BN * D / 256;        // coordinates a thread
+        constexpr int PER = D / DP;             // threads a row
+        const int dt = threadIdx.x - 256, r = dt / PER, x0 = (dt % PER) * DP;
+        const int* table = P.table + (long long)b * P.max_pages;
+        const bool lo = P.sfmt == SRFTKV_SCALE_FP32;
+        auto row_of = [&](int t) -> long long {  // packed row of this thread's token in tile t, -1: none
+            const int tok = (ta + t) * BN + r;
+            if (t >= n || tok >= len) return -1;
+            const int pg = __ldg(table + (tok >> P.lg_page));
+            if ((unsigned)pg >= (unsigned)P.n_pages) {
+                atomicOr(P.fault, kFaultPage);
+                return -1;
+            }
+            return ((((long long)pg * P.Hkv + h) << P.lg_page) | (tok & ((1 << P.lg_page) - 1)));
+        };
+        tile::Piece<DP> pk, pv;
+        long long row = row_of(0);
+        tile::load_piece<D, DP>(P.kc, P.ks, row, x0, W.bits_k, P.sfmt, P.lg_group, pk);
+        tile::load_piece<D, DP>(P.vc, P.vs, row, x0, W.bits_v, P.sfmt, P.lg_group, pv);
+        row = row_of(1);
+        for (int t = 0; t < n; ++t) {
+            const int st = t & 1;
+            if (t >= 2 && !wait(K_EMPTY + st, ((t >> 1) - 1) & 1)) break;
+            tile::store_piece_any<D, BN, DP>(smem + C::OFF_K + st * C::TB, r, x0, W.bits_k, lo, pk);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(K_FULL + st));
+            tile::load_piece<D, DP>(P.kc, P.ks, row, x0, W.bits_k, P.sfmt, P.lg_group, pk);
+            if (t >= 2 && !wait(V_EMPTY + st, ((t >> 1) - 1) & 1)) break;
+            tile::store_piece_any<D, BN, DP>(smem + C::OFF_V + st * C::TB, r, x0, W.bits_v, lo, pv);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(V_FULL + st));
+            tile::load_piece<D, DP>(P.vc, P.vs, row, x0, W.bits_v, P.sfmt, P.lg_group, pv);
+            row = row_of(t + 2);
+        }
+        if (W.n_parts == 1 && !failed) {
+            // R_s for the way back, where the K tiles were (d = 256: and the V tiles), once their last MMAs are done:
+            // rows n of 64 inputs, the MN-major B operand
+            for (int t = max(0, n - 2); t < n; ++t) {
+                wait(K_EMPTY + (t & 1), (t >> 1) & 1);
+                if (NQ == 1) wait(V_EMPTY + (t & 1), (t >> 1) & 1);
+            }
+            if (!failed) {
+                for (int c = dt; c < D * (D / 8); c += 256) {
+                    const int nr = c / (D / 8), ch = c % (D / 8);
+                    uint4 hi, unused;
+                    tile::r_chunk<D, false>(nr, 8 * ch, P.tr_v == SRFTKV_TRANSFORM_SRHT, tw, sg, hi, unused);
+                    *reinterpret_cast<uint4*>(smem + C::OFF_K + (ch >> 3) * (D * 128) + nr * 128 +
+                                              (((ch & 7) ^ (nr & 7)) << 4)) = hi;
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(R_FULL));
+            }
+        }
+    } else if (!failed && lane == 0) {
+        // =========================== MMA ===========================
+        auto issue_s = [&](int sb, int qt, int t) {
+            const uint32_t kb = sbase + C::OFF_K + (t & 1) * C::TB;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                tc::mma_f16(tmem + sb * C::S_STEP, tc::sw128_desc(sbase + qt * C::QB + (ks >> 2) * 16384 + (ks & 3) * 32),
+                            tc::sw128_desc(kb + (ks >> 2) * (BN * 128) + (ks & 3) * 32), tile::idesc(128, BN, false), ks > 0);
+        };
+        auto issue_pv = [&](int sb, int oc, int t, bool first) {
+            const uint32_t vb = sbase + C::OFF_V + (t & 1) * C::TB;
+#pragma unroll
+            for (int ks = 0; ks < BN / 16; ++ks)
+                tc::mma_f16_ta(tmem + C::O_COL + oc, tmem + C::P_COL + sb * C::P_STEP + 8 * ks, tile::desc_mn(vb + ks * 2048, BN * 128),
+                               tile::idesc(128, D, true), !(first && ks == 0));
+        };
+        if constexpr (NQ == 2) {
+            auto start_s = [&](int i, int j) -> bool {  // S of stream i, step j; false: a wait ran out
+                const int t = dual ? 2 * j + i : j;
+                if (t >= n) return true;
+                if ((i == 0 || dual) && !wait1(K_FULL + (t & 1), (t >> 1) & 1)) return false;
+                tc::fence_after_sync();
+                issue_s(i, dual ? 0 : i, t);
+                if (i == 1 || dual) tc::commit(bar(K_EMPTY + (t & 1)));
+                tc::commit(bar(S_FULL + i));
+                return true;
+            };
+            bool ok = start_s(0, 0) && start_s(1, 0);
+            for (int j = 0; ok && j < n0; ++j)
+                for (int i = 0; ok && i < 2; ++i) {
+                    const int t = dual ? 2 * j + i : j;
+                    if (t >= n) continue;
+                    ok = (i == 1 && !dual || wait1(V_FULL + (t & 1), (t >> 1) & 1)) && wait1(P_FULL + i, j & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    issue_pv(i, i * D, t, j == 0);
+                    tc::commit(bar(PV_DONE + i));
+                    if (i == 1 || dual) tc::commit(bar(V_EMPTY + (t & 1)));
+                    ok = start_s(i, j + 1);
+                }
+        } else {
+            auto start_s = [&](int t) -> bool {
+                if (t >= n) return true;
+                if (!wait1(K_FULL + (t & 1), (t >> 1) & 1)) return false;
+                tc::fence_after_sync();
+                issue_s(t & 1, 0, t);
+                tc::commit(bar(K_EMPTY + (t & 1)));
+                tc::commit(bar(S_FULL + (t & 1)));
+                return true;
+            };
+            bool ok = start_s(0) && start_s(1);
+            for (int t = 0; ok && t < n; ++t) {
+                ok = wait1(V_FULL + (t & 1), (t >> 1) & 1) && wait1(P_FULL + (t & 1), (t >> 1) & 1);
+                if (!ok) break;
+                tc::fence_after_sync();
+                issue_pv(t & 1, 0, t, t == 0);
+                tc::commit(bar(PV_DONE));
+                tc::commit(bar(V_EMPTY + (t & 1)));
+                ok = start_s(t + 2);
+            }
+        }
+        if (W.n_parts == 1 && !failed && wait1(R_FULL, 0) && wait1(EP_FULL, 0)) {
+            tc::fence_after_sync();
+            for (int i = 0; i < NQ; ++i)
+#pragma unroll 1
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc::mma_f16(tmem + i * 128, tc::sw128_desc(sbase + i * C::QB + (ks >> 2) * 16384 + (ks & 3) * 32),
+                                tile::desc_mn(sbase + C::OFF_K + ks * 2048, D * 128), tile::idesc(128, D, true), ks > 0);
+            tc::commit(bar(OUT_FULL));
+        }
+    }
+    if (failed) atomicOr(P.fault, kFaultWait);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 16) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+static int launch_tile(const PagedAttnParams& P, const TileWork& W, int blocks, cudaStream_t stream) {
+    using C = tile::Cfg<D>;
+    cudaError_t e = cudaFuncSetAttribute(paged_attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess) {
+        paged_attn_tile_kernel<D><<<dim3(P.B * P.Hkv, blocks, W.n_splits), tile::THREADS, C::SMEM, stream>>>(P, W);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) {
+        set_error("paged attention launch failed: %s", cudaGetErrorString(e));
+        return SRFTKV_ERR_CUDA;
+    }
+    return SRFTKV_OK;
+}
+
+}  // namespace srftkv
