@@ -78,6 +78,26 @@ struct TileWork {
 int launch_tile64(const PagedAttnParams& P, const TileWork& W, int blocks, cudaStream_t s);
 int launch_tile128(const PagedAttnParams& P, const TileWork& W, int blocks, cudaStream_t s);
 int launch_tile256(const PagedAttnParams& P, const TileWork& W, int blocks, cudaStream_t s);
+// The same for the split kernel (paged_attn_split.cuh)
+struct SplitWork {
+    int nr;        // groups of four query rows a CTA
+    int groups;    // CTAs a (sequence, kv head, split): its rows / (4 nr)
+    int n_splits, n_parts;
+    int tokens;    // of a split, a multiple of 128
+    int chunks;    // the same in chunks of the instance (set at its launch)
+    int bits_k, bits_v, dtype;
+    float* part_ml;
+    float* part_acc;
+};
+int launch_split64_fp32(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s);
+int launch_split64_fp16(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s);
+int launch_split64_e8m0(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s);
+int launch_split128_fp32(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s);
+int launch_split128_fp16(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s);
+int launch_split128_e8m0(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s);
+int launch_split256_fp32(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s);
+int launch_split256_fp16(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s);
+int launch_split256_e8m0(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s);
 size_t paged_attention_workspace(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window);
 int paged_attention(const PagedAttnCall& c);
 unsigned int paged_attn_take_fault();

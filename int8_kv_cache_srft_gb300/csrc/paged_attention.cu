@@ -8,6 +8,7 @@
 // out = R^T (o / lambda_V).
 #include <algorithm>
 
+#include "attn_frag.cuh"
 #include "paged.h"
 #include "paged_rotate.cuh"
 
@@ -24,6 +25,7 @@ __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_co
                                                                  const float* __restrict__ part_acc) {
     constexpr int E = D / 32;
     __shared__ float2 sm[4][D / 2];
+    griddep_wait();  // the partial results first
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y;
     const long long u = (long long)blockIdx.x * 4 + warp;
@@ -65,37 +67,57 @@ __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_co
 
 // How a call is divided: a pure function of its sizes (the workspace size and the launch both ask for it).
 struct Plan {
+    bool few;        // the split kernel; else the tile kernel
+    SplitWork S;
     TileWork W;
-    int blocks;      // row blocks a (sequence, kv head)
+    int blocks;      // tile kernel: row blocks a (sequence, kv head)
+    int n_parts;     // partial results a row; 1: written as the answer at once
     size_t acc_off;  // part_ml at 0, part_acc here
     size_t bytes;
 };
 static Plan make_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window) {
     Plan p = {};
-    const int rep = Hq / Hkv, bn = d == 256 ? 64 : 128;
-    const long long rows = (long long)max_q * rep;
-    p.W.dual = d != 256 && rows <= 128;
-    p.W.rows_per_block = d == 256 || p.W.dual ? 128 : 256;
-    p.blocks = (int)((rows + p.W.rows_per_block - 1) / p.W.rows_per_block);
-    // the most tiles any block sees
-    long long see = max_len;
-    if (window) see = std::min<long long>(see, (long long)window + (p.W.rows_per_block - 1) / rep + 1);
-    long long tiles = (see + bn - 1) / bn;
-    if (window) tiles = std::min<long long>((max_len + bn - 1) / bn, tiles + 1);
-    // one CTA runs on an SM: split the cache where that shortens waves * (tiles a split + the fixed part)
-    const long long base = (long long)B * Hkv * p.blocks, sms = device_sm_count(), fixed = 6;
-    long long best = 1, best_cost = -1;
-    for (long long s = 1; s <= std::min<long long>(tiles, 64); ++s) {
-        const long long tps = (tiles + s - 1) / s;
-        if (s > 1 && (tiles + tps - 1) / tps != s) continue;
-        const long long cost = (base * s + sms - 1) / sms * (tps + fixed);
-        if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
+    const int rep = Hq / Hkv;
+    const long long rows = (long long)max_q * rep, sms = device_sm_count();
+    p.few = rows <= 8;
+    if (p.few) {
+        p.S.nr = rows > 4 && d <= 128 ? 2 : 1;
+        p.S.groups = (int)((rows + 4 * p.S.nr - 1) / (4 * p.S.nr));
+        // tokens any row group sees, with the chunk its window starts inside
+        long long see = max_len;
+        if (window) see = std::min<long long>(see, (long long)window + max_q - 1 + 31);
+        const long long base = (long long)B * Hkv * p.S.groups;
+        long long s = (16 * sms + base - 1) / base;
+        s = std::max(1ll, std::min(s, (see + 255) / 256));
+        long long tokens = ((see + s - 1) / s + 127) / 128 * 128;
+        p.S.tokens = (int)tokens;
+        p.S.n_splits = (int)((see + tokens - 1) / tokens);
+        p.n_parts = p.S.n_parts = p.S.n_splits;
+    } else {
+        const int bn = d == 256 ? 64 : 128;
+        p.W.dual = d != 256 && rows <= 128;
+        p.W.rows_per_block = d == 256 || p.W.dual ? 128 : 256;
+        p.blocks = (int)((rows + p.W.rows_per_block - 1) / p.W.rows_per_block);
+        // the most tiles any block sees
+        long long see = max_len;
+        if (window) see = std::min<long long>(see, (long long)window + (p.W.rows_per_block - 1) / rep + 1);
+        long long tiles = (see + bn - 1) / bn;
+        if (window) tiles = std::min<long long>((max_len + bn - 1) / bn, tiles + 1);
+        // one CTA runs on an SM: split the cache where that shortens waves * (tiles a split + the fixed part)
+        const long long base = (long long)B * Hkv * p.blocks, fixed = 6;
+        long long best = 1, best_cost = -1;
+        for (long long s = 1; s <= std::min<long long>(tiles, 64); ++s) {
+            const long long tps = (tiles + s - 1) / s;
+            if (s > 1 && (tiles + tps - 1) / tps != s) continue;
+            const long long cost = (base * s + sms - 1) / sms * (tps + fixed);
+            if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
+        }
+        p.W.n_splits = (int)best;
+        p.W.tps = (int)((tiles + best - 1) / best);
+        p.n_parts = p.W.n_parts = p.W.n_splits * (p.W.dual ? 2 : 1);
     }
-    p.W.n_splits = (int)best;
-    p.W.tps = (int)((tiles + best - 1) / best);
-    p.W.n_parts = p.W.n_splits * (p.W.dual ? 2 : 1);
-    if (p.W.n_parts > 1) {
-        const size_t n = (size_t)total_q * Hq * p.W.n_parts;
+    if (p.n_parts > 1) {
+        const size_t n = (size_t)total_q * Hq * p.n_parts;
         p.acc_off = (n * 8 + 255) / 256 * 256;
         p.bytes = p.acc_off + n * d * 4;
     }
@@ -108,12 +130,19 @@ size_t paged_attention_workspace(int d, int Hq, int Hkv, int B, int total_q, int
 }
 
 template <int D>
-static void launch_combine(const PagedAttnCall& c, const PagedAttnParams& P, const TileWork& W) {
-    const dim3 grid((unsigned)(((long long)P.max_q * P.Hq + 3) / 4), P.B);
-    if (c.dtype == SRFTKV_DTYPE_BF16)
-        paged_attn_combine_kernel<D, __nv_bfloat16><<<grid, 128, 0, c.stream>>>(P, W.n_parts, W.part_ml, W.part_acc);
-    else
-        paged_attn_combine_kernel<D, __half><<<grid, 128, 0, c.stream>>>(P, W.n_parts, W.part_ml, W.part_acc);
+static cudaError_t launch_combine(const PagedAttnCall& c, const PagedAttnParams& P, int n_parts, const float* ml,
+                                  const float* acc) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)P.max_q * P.Hq + 3) / 4), P.B);
+    cfg.blockDim = dim3(128);
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[1];  // it may start while the kernel before it ends, and waits for it on the device
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto* k = c.dtype == SRFTKV_DTYPE_BF16 ? paged_attn_combine_kernel<D, __nv_bfloat16> : paged_attn_combine_kernel<D, __half>;
+    return cudaLaunchKernelEx(&cfg, k, P, n_parts, ml, acc);
 }
 
 int paged_attention(const PagedAttnCall& c) {
@@ -123,25 +152,39 @@ int paged_attention(const PagedAttnCall& c) {
     if (symbol_address(cache, &g_paged_attn_fault, &f, "the paged attention's fault word")) return SRFTKV_ERR_CUDA;
     P.fault = static_cast<unsigned int*>(f);
     Plan plan = make_plan(c.d, P.Hq, P.Hkv, P.B, P.total_q, P.max_q, P.max_len, P.window);
-    TileWork& W = plan.W;
-    W.bits_k = c.bits_k;
-    W.bits_v = c.bits_v;
-    W.dtype = c.dtype;
-    W.part_ml = static_cast<float*>(c.workspace);
-    W.part_acc = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + plan.acc_off);
-    const int rc = c.d == 64    ? launch_tile64(P, W, plan.blocks, c.stream)
-                   : c.d == 128 ? launch_tile128(P, W, plan.blocks, c.stream)
-                                : launch_tile256(P, W, plan.blocks, c.stream);
-    if (rc) return rc;
-    if (W.n_parts > 1) {
-        if (c.d == 64) launch_combine<64>(c, P, W);
-        else if (c.d == 128) launch_combine<128>(c, P, W);
-        else launch_combine<256>(c, P, W);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) {
-            set_error("paged attention launch failed: %s", cudaGetErrorString(e));
-            return SRFTKV_ERR_CUDA;
-        }
+    float* ml = static_cast<float*>(c.workspace);
+    float* acc = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + plan.acc_off);
+    int rc;
+    if (plan.few) {
+        SplitWork& S = plan.S;
+        S.bits_k = c.bits_k;
+        S.bits_v = c.bits_v;
+        S.dtype = c.dtype;
+        S.part_ml = ml;
+        S.part_acc = acc;
+        using Fn = int (*)(const PagedAttnParams&, const SplitWork&, cudaStream_t);
+        static const Fn fn[3][3] = {{launch_split64_fp32, launch_split64_fp16, launch_split64_e8m0},
+                                    {launch_split128_fp32, launch_split128_fp16, launch_split128_e8m0},
+                                    {launch_split256_fp32, launch_split256_fp16, launch_split256_e8m0}};
+        rc = fn[c.d == 64 ? 0 : c.d == 128 ? 1 : 2][P.sfmt](P, S, c.stream);
+    } else {
+        TileWork& W = plan.W;
+        W.bits_k = c.bits_k;
+        W.bits_v = c.bits_v;
+        W.dtype = c.dtype;
+        W.part_ml = ml;
+        W.part_acc = acc;
+        rc = c.d == 64    ? launch_tile64(P, W, plan.blocks, c.stream)
+             : c.d == 128 ? launch_tile128(P, W, plan.blocks, c.stream)
+                          : launch_tile256(P, W, plan.blocks, c.stream);
+    }
+    if (rc || plan.n_parts == 1) return rc;
+    const cudaError_t e = c.d == 64    ? launch_combine<64>(c, P, plan.n_parts, ml, acc)
+                          : c.d == 128 ? launch_combine<128>(c, P, plan.n_parts, ml, acc)
+                                       : launch_combine<256>(c, P, plan.n_parts, ml, acc);
+    if (e != cudaSuccess) {
+        set_error("paged attention launch failed: %s", cudaGetErrorString(e));
+        return SRFTKV_ERR_CUDA;
     }
     return SRFTKV_OK;
 }

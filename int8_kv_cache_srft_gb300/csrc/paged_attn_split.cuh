@@ -1,0 +1,718 @@
+// paged_attn_split.cuh -- attention of a few query rows over the paged cache:
+// one token (or a few) a sequence, where the bytes of the cache are the cost.
+//
+// Grid (splits, sequence and kv head, row groups).  A CTA's 4 NR query rows
+// (query tokens times the heads of its kv head) share every byte it reads.
+// Each of its four warps streams every fourth chunk of CH tokens of the split
+// into its own ring of shared-memory stages (a swizzled TMA box a page for the
+// codes, a plain bulk copy for the scales, NS stages) and keeps its own online
+// softmax; the warps meet in shared memory at the end.
+//
+//   S = codes_K . q~  with mma.sync m16n8k16: codes as exact fp16 (offset-binary
+//       subnormals, attn_frag.cuh), 16 tokens a tile; columns 2c, 2c+1 carry
+//       row c's two 16-dim groups of a 32-dim chunk (8-bit keys: column 2c
+//       alone), so the group scale multiplies the fp32 partial, K rounded
+//       nowhere.
+//   acc += codes_V^T . (p scale_V), the offset taken out by a second
+//       contraction of the same operand with the constant -8 (-128), so the
+//       accumulators never hold more than a tile's worth of it.
+//
+// The cache is read as it is and never turned back: q is rotated here (one warp
+// a row, while the first chunks are on their way), the sum on the way out.
+// What bounds it: the bytes of the cache at 4-bit codes; the logic ops that
+// turn codes into operands are next.
+//
+// Roundings: q~ to fp16 (with one row group at d <= 128 as hi + lo, about 22
+// bits); p scale_V to fp16 (with fp16 scales p is rounded before the product
+// too).  p is at most 2^2 beside 4-bit and 2^6 beside 8-bit codes: code * scale
+// below 65504 keeps p scale_V finite, and small scales above fp16's subnormals.
+#pragma once
+
+#include <cstring>
+
+#include "attn_frag.cuh"
+#include "paged.h"
+#include "paged_rotate.cuh"
+#include "ptx.cuh"
+
+namespace srftkv {
+
+namespace split {
+
+constexpr int WARPS = 4;
+
+template <int SF>
+constexpr int sbytes() { return SF == SRFTKV_SCALE_FP32 ? 4 : SF == SRFTKV_SCALE_FP16 ? 2 : 1; }
+constexpr int up(int v, int a) { return (v + a - 1) / a * a; }
+
+// A plane of code rows in shared memory: rows of up to 128 bytes, swizzled by TMA with the mode of their length;
+// 256-byte rows as two 128-byte halves one after the other
+template <int RB, int CH>
+struct Plane {
+    static constexpr int R = RB < 128 ? RB : 128, HALVES = RB / R, BYTES = CH * RB;
+    static __device__ __forceinline__ int swz(int r) { return ((r * R) >> 7) & (R / 16 - 1); }
+};
+template <int D, int BK, int BV, int SF>
+struct Cfg {
+    static constexpr int RK = D * BK / 8, RV = D * BV / 8, SR = D / 16 * sbytes<SF>();  // row bytes (scales: at most)
+    static constexpr int CH = 32 * (RK + RV + 2 * SR) <= 9216 ? 32 : 16;                // tokens a chunk
+    static constexpr int OFF_V = up(CH * RK, 1024), OFF_KS = OFF_V + up(CH * RV, 1024);
+    static constexpr int OFF_VS = OFF_KS + up(CH * SR, 128);
+    static constexpr int STAGE = up(OFF_VS + CH * SR, 1024);
+    static constexpr int NS = WARPS * 3 * STAGE <= 74 * 1024 ? 3 : 2;
+};
+template <int D, int BK, int BV, int SF, int NR>
+struct Smem {
+    using C = Cfg<D, BK, BV, SF>;
+    static constexpr int ROWS = 4 * NR;
+    static constexpr int RING = WARPS * C::NS * C::STAGE;
+    static constexpr int MERGE = WARPS * ROWS * (D + 2) * 4;      // over the ring, at the end
+    static constexpr int BODY = up(RING > MERGE ? RING : MERGE, 16);
+    static constexpr int OFF_Q = BODY;                            // q~ rows
+    static constexpr int OFF_ROT = OFF_Q + ROWS * D * 4;          // a warp's rotation scratch
+    static constexpr int OFF_BAR = OFF_ROT + WARPS * D * 4;
+    static constexpr int BYTES = OFF_BAR + WARPS * C::NS * 16 + 1024;
+};
+
+// scale f (16-dim unit) of staged row r; ng: scales a row
+template <int SF>
+__device__ __forceinline__ float scale_at(const uint8_t* s, int r, int f, int ng, int lg) {
+    const int i = r * ng + (lg == 4 ? f : (16 * f) >> lg);
+    if constexpr (SF == SRFTKV_SCALE_FP32) return reinterpret_cast<const float*>(s)[i];
+    else if constexpr (SF == SRFTKV_SCALE_FP16) return __half2float(reinterpret_cast<const __half*>(s)[i]);
+    else return __uint_as_float((uint32_t)s[i] << 23);
+}
+// scales of units 4p .. 4p+3 of staged row r
+template <int SF>
+__device__ __forceinline__ void scales4(const uint8_t* s, int r, int p, int ng, int lg, float (&v)[4]) {
+    if (lg == 4) {
+        if constexpr (SF == SRFTKV_SCALE_FP32) {
+            const float4 f = *reinterpret_cast<const float4*>(s + (r * ng + 4 * p) * 4);
+            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+        } else if constexpr (SF == SRFTKV_SCALE_FP16) {
+            const uint2 w = *reinterpret_cast<const uint2*>(s + (r * ng + 4 * p) * 2);
+            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+            v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+        } else {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(s + r * ng + 4 * p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = scale_at<SF>(s, r, 4 * p + i, ng, lg);
+    }
+}
+__device__ __forceinline__ uint32_t h2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+}  // namespace split
+
+template <int D, int BK, int BV, int SF, int NR>
+__global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
+    paged_attn_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                            const __grid_constant__ PagedAttnParams P, const __grid_constant__ SplitWork W) {
+    using C = split::Cfg<D, BK, BV, SF>;
+    using M = split::Smem<D, BK, BV, SF, NR>;
+    using PK = split::Plane<C::RK, C::CH>;
+    using PV = split::Plane<C::RV, C::CH>;
+    constexpr int CH = C::CH, NT = CH / 16, NS = C::NS, NP = D / 64, E = D / 32;
+    constexpr bool LO = NR == 1 && D <= 128;
+    constexpr float PBITS = BV == 4 ? 2.f : 6.f;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int g = lane >> 2, c = lane & 3;
+
+    // ---- rows and chunks of this CTA ----
+    const int b = blockIdx.y / P.Hkv, h = blockIdx.y - b * P.Hkv, spl = blockIdx.x;
+    const int q0 = P.cu_q ? P.cu_q[b] : b;
+    int m_tok = min(P.cu_q ? P.cu_q[b + 1] - q0 : 1, P.max_q);
+    if (q0 < 0) m_tok = 0;
+    m_tok = min(m_tok, P.total_q - q0);
+    const int row0 = blockIdx.z * M::ROWS, n_rows = min(m_tok * P.rep - row0, M::ROWS);
+    if (n_rows <= 0) return;
+    const int len = min(max(P.seq_lens[b], 0), P.max_len);
+    const int pos_lo = len - m_tok + row0 / P.rep, pos_hi = len - m_tok + (row0 + n_rows - 1) / P.rep;
+    auto row_at = [&](int r) -> long long {  // row r of the group in [total_q * Hq]
+        const int i = (row0 + r) / P.rep;
+        return (long long)(q0 + i) * P.Hq + h * P.rep + (row0 + r - i * P.rep);
+    };
+    auto row_ptr = [&](const void* base, long long stride, int r) -> long long {  // element offset of row r of q / out
+        const int i = (row0 + r) / P.rep;
+        return (q0 + i) * stride + (long long)(h * P.rep + (row0 + r - i * P.rep)) * D;
+    };
+    const int first_chunk = P.window ? max(0, pos_lo - P.window + 1) / CH : 0;
+    const int c_begin = first_chunk + spl * W.chunks;
+    const int c_end = min(pos_hi >= 0 ? pos_hi / CH + 1 : 0, c_begin + W.chunks);
+    if (c_begin >= c_end) {  // nothing visible here: zeros, or empty partials
+        for (int r = threadIdx.x; r < n_rows; r += blockDim.x) {
+            if (W.n_parts == 1) {
+                uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + row_ptr(P.out, P.out_stride, r));
+                for (int k = 0; k < D / 8; ++k) o[k] = make_uint4(0, 0, 0, 0);
+            } else {
+                float* ml = W.part_ml + (row_at(r) * W.n_parts + spl) * 2;
+                ml[0] = -INFINITY;
+                ml[1] = 0.f;
+            }
+        }
+        griddep_launch_dependents();
+        return;
+    }
+
+    // ---- the ring: barriers and bad-page masks of this warp's stages ----
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::OFF_BAR) + warp * NS;
+    uint32_t* bad = reinterpret_cast<uint32_t*>(smem + M::OFF_BAR + split::WARPS * NS * 8) + warp * NS;
+    uint8_t* ring = smem + warp * NS * C::STAGE;
+    if (lane == 0) {
+        for (int s = 0; s < NS; ++s) ptx::mbar_init(ptx::smem_u32(&bars[s]), 1);
+        ptx::fence_barrier_init();
+    }
+    __syncwarp();
+    const int ng = D >> P.lg_group, srb = ng * split::sbytes<SF>();
+    const int box = min(CH, 1 << P.lg_page), boxes = CH / box;  // tokens of a chunk that lie in one page
+    const int* table = P.table + (long long)b * P.max_pages;
+    const int psize = 1 << P.lg_page;
+    // one lane's copies of a chunk into stage s: the pages that hold its tokens below len
+    auto issue = [&](int chunk, int s) {
+        const uint32_t bar = ptx::smem_u32(&bars[s]);
+        uint8_t* st = ring + s * C::STAGE;
+        const int t0 = chunk * CH, n_box = min(boxes, (len - t0 + box - 1) / box);
+        ptx::mbar_arrive_expect_tx(bar, n_box * box * (C::RK + C::RV + 2 * srb));
+        uint32_t mask = 0;
+        for (int x = 0; x < n_box; ++x) {
+            const int t = t0 + x * box;
+            int pg = __ldg(table + (t >> P.lg_page));
+            if ((unsigned)pg >= (unsigned)P.n_pages) {
+                mask |= 1u << x;
+                pg = 0;
+                atomicOr(P.fault, kFaultPage);
+            }
+            const int ph = pg * P.Hkv + h, off = t & (psize - 1);
+            const long long row = (long long)ph * psize + off;
+#pragma unroll
+            for (int hv = 0; hv < PK::HALVES; ++hv)
+                ptx::tma_load_3d(ptx::smem_u32(st + hv * (CH * 128) + x * box * PK::R), &tm_k, bar, hv * 128, off, ph);
+#pragma unroll
+            for (int hv = 0; hv < PV::HALVES; ++hv)
+                ptx::tma_load_3d(ptx::smem_u32(st + C::OFF_V + hv * (CH * 128) + x * box * PV::R), &tm_v, bar, hv * 128, off, ph);
+            ptx::bulk_load(ptx::smem_u32(st + C::OFF_KS + x * box * srb), P.ks + row * srb, box * srb, bar);
+            ptx::bulk_load(ptx::smem_u32(st + C::OFF_VS + x * box * srb), P.vs + row * srb, box * srb, bar);
+        }
+        bad[s] = mask;
+    };
+    // bad[] is written after the arrival here, so a stage's mask is ordered for the other lanes by the __syncwarp
+    // that follows every issue
+    if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < NS - 1; ++j)
+            if (c_begin + warp + j * split::WARPS < c_end) issue(c_begin + warp + j * split::WARPS, j);
+    }
+    __syncwarp();
+
+    // ---- q~ = R q sm_scale log2 e / lambda_K, one warp a row ----
+    float* qs = reinterpret_cast<float*>(smem + M::OFF_Q);
+    float2* scratch = reinterpret_cast<float2*>(smem + M::OFF_ROT) + warp * (D / 2);
+#pragma unroll 1
+    for (int r = warp; r < M::ROWS; r += split::WARPS) {
+        float v[E] = {};
+        if (r < n_rows) {
+            const uint16_t* src = static_cast<const uint16_t*>(P.q) + row_ptr(P.q, P.q_stride, r);
+            if (W.dtype == SRFTKV_DTYPE_BF16) rot::load_row<D>(reinterpret_cast<const __nv_bfloat16*>(src), lane, v);
+            else rot::load_row<D>(reinterpret_cast<const __half*>(src), lane, v);
+            rot::forward<D>(v, lane, P.tr_k, P.sign_mask, scratch);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] *= P.qscale;
+            if (P.lam_k) {
+                float l[E];
+                rot::load_lambda<D>(P.lam_k + (long long)h * D, lane, l);
+#pragma unroll
+                for (int j = 0; j < E; ++j) v[j] = __fdiv_rn(v[j], l[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < E; ++j) qs[r * D + E * lane + j] = v[j];
+    }
+    __syncthreads();
+
+    // ---- K-side B fragments: column g = (row g/2, half g%2); nb: the accumulator's start, minus the code offset
+    // times the column sum, for this thread's columns 2c, 2c+1 ----
+    constexpr int NB = D / 16;
+    uint32_t qh[NR][D / 8], ql[LO ? NR : 1][LO ? D / 8 : 1];
+    float nb[NR][NB];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+        const float* q = qs + (4 * nr + (g >> 1)) * D;
+        if constexpr (BK == 4) {
+            const float on = (c >> 1) == (g & 1) ? 1.f : 0.f;
+#pragma unroll
+            for (int mm = 0; mm < D / 32; ++mm) {
+                // thread c: dims 8c .. 8c+7 of the chunk; pairs (j, j+4), the high-nibble rows with q / 16
+                const float4 a = *reinterpret_cast<const float4*>(q + 32 * mm + 8 * c);
+                const float4 e = *reinterpret_cast<const float4*>(q + 32 * mm + 8 * c + 4);
+                const float x[4] = {a.x * on, a.y * on, a.z * on, a.w * on}, y[4] = {e.x * on, e.y * on, e.z * on, e.w * on};
+                float part = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float u = (j & 1) ? 0.0625f : 1.f;
+                    if constexpr (LO) {
+                        split_h2(x[j] * u, y[j] * u, qh[nr][4 * mm + j], ql[nr][4 * mm + j]);
+                        part += (h2_sum(qh[nr][4 * mm + j]) + h2_sum(ql[nr][4 * mm + j])) * ((j & 1) ? 16.f : 1.f);
+                    } else {
+                        qh[nr][4 * mm + j] = split::h2(x[j] * u, y[j] * u);
+                        part += h2_sum(qh[nr][4 * mm + j]) * ((j & 1) ? 16.f : 1.f);
+                    }
+                }
+                part += __shfl_xor_sync(0xffffffffu, part, 1);
+                part += __shfl_xor_sync(0xffffffffu, part, 2);
+                nb[nr][2 * mm] = (-8.f / kSub) * __shfl_sync(0xffffffffu, part, 8 * c);
+                nb[nr][2 * mm + 1] = (-8.f / kSub) * __shfl_sync(0xffffffffu, part, 8 * c + 4);
+            }
+        } else {
+            const float on = (g & 1) ? 0.f : 1.f;
+#pragma unroll
+            for (int mm = 0; mm < D / 16; ++mm) {  // thread c: dims 4c .. 4c+3; pairs (j, j+2)
+                const float4 a = *reinterpret_cast<const float4*>(q + 16 * mm + 4 * c);
+                float part;
+                if constexpr (LO) {
+                    split_h2(a.x * on, a.z * on, qh[nr][2 * mm], ql[nr][2 * mm]);
+                    split_h2(a.y * on, a.w * on, qh[nr][2 * mm + 1], ql[nr][2 * mm + 1]);
+                    part = h2_sum(qh[nr][2 * mm]) + h2_sum(ql[nr][2 * mm]) + h2_sum(qh[nr][2 * mm + 1]) + h2_sum(ql[nr][2 * mm + 1]);
+                } else {
+                    qh[nr][2 * mm] = split::h2(a.x * on, a.z * on);
+                    qh[nr][2 * mm + 1] = split::h2(a.y * on, a.w * on);
+                    part = h2_sum(qh[nr][2 * mm]) + h2_sum(qh[nr][2 * mm + 1]);
+                }
+                part += __shfl_xor_sync(0xffffffffu, part, 1);
+                part += __shfl_xor_sync(0xffffffffu, part, 2);
+                nb[nr][mm] = (-128.f / kSub) * __shfl_sync(0xffffffffu, part, 8 * c);
+            }
+        }
+    }
+
+    float acc[NR][D / 4], mx[NR], l[NR];
+    int pos[NR], low[NR];  // row c of each group: the last and first position it sees
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) acc[nr][i] = 0.f;
+        mx[nr] = -INFINITY;
+        l[nr] = 0.f;
+        const int r = 4 * nr + c;
+        pos[nr] = r < n_rows ? len - m_tok + (row0 + r) / P.rep : -1;  // rows past the last see nothing
+        low[nr] = P.window ? pos[nr] - P.window + 1 : 0;
+    }
+    // per-lane ldmatrix rows: 8-row groups (0-7 | 8-15) x (chunk | chunk + 1)
+    const int rl = (lane & 7) + ((lane >> 3) & 1) * 8, dl = lane >> 4;
+    const uint32_t ko = rl * PK::R, kx = (uint32_t)(dl ^ PK::swz(rl)) << 4;
+    const uint32_t vo = rl * PV::R, vx = (uint32_t)(dl ^ PV::swz(rl)) << 4;
+    auto plane_at = [](uint32_t base, uint32_t off, uint32_t x16, int R, int tr, int seg) -> uint32_t {
+        const int per = R / 16;  // 16-byte chunks a (half) row
+        return base + (seg / per) * (CH * 128) + off + tr * R + (((uint32_t)(seg % per) << 4) ^ x16);
+    };
+
+    bool failed = false, undrained = false;
+    int it = 0;
+    for (int chunk = c_begin + warp; chunk < c_end; chunk += split::WARPS, ++it) {
+        const int s = it % NS, nxt = chunk + (NS - 1) * split::WARPS;
+        if (lane == 0 && nxt < c_end) issue(nxt, (it + NS - 1) % NS);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(ptx::smem_u32(&bars[s]), (it / NS) & 1))) {
+            if (lane == 0) {
+                atomicOr(P.fault, kFaultWait);
+                bool all = true;  // this warp's copies in flight land before its shared memory is used for anything else
+                for (int j = 0; j < NS; ++j)
+                    if (chunk + j * split::WARPS < c_end)
+                        all &= ptx::mbar_wait_bounded(ptx::smem_u32(&bars[(it + j) % NS]), ((it + j) / NS) & 1, 1u << 16);
+                undrained = !all;
+            }
+            undrained = __shfl_sync(0xffffffffu, undrained, 0);
+            failed = true;
+            break;
+        }
+        uint8_t* st = ring + s * C::STAGE;
+        const uint32_t kb = ptx::smem_u32(st), vb = ptx::smem_u32(st + C::OFF_V);
+        uint8_t *ks = st + C::OFF_KS, *vs = st + C::OFF_VS;
+        const int t0 = chunk * CH, have = len - t0;
+        const uint32_t bad_mask = bad[s];
+        if (have < CH || bad_mask) {
+            // rows past the end may hold anything: their scales become zeros (p is zero there, and zero times
+            // anything but a NaN or an infinity); so do a bad page's rows, K and V
+            for (int r = lane; r < CH; r += 32) {
+                const bool gone = (bad_mask >> (r / box)) & 1;
+                if (r >= have || gone)
+                    for (int k = 0; k < srb; ++k) {
+                        vs[r * srb + k] = 0;
+                        ks[r * srb + k] = 0;
+                    }
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+        }
+        // ---- scores: sc[nr][st][r] of row c, token 16 st + g + 8 r, in units of 2^-24 ----
+        float sc[NR][NT][2];
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt) {
+            const int tr = 16 * tt;
+            float2 a0[NR], a1[NR];
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) a0[nr] = a1[nr] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                float s0[4], s1[4];
+                split::scales4<SF>(ks, tr + g, p, ng, P.lg_group, s0);
+                split::scales4<SF>(ks, tr + g + 8, p, ng, P.lg_group, s1);
+                if constexpr (BK == 4) {
+                    uint32_t r[4];
+                    ldsm_x4(plane_at(kb, ko, kx, PK::R, tr, 2 * p), r);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int mm = 2 * p + e;
+                        const uint32_t rg = ob4(r[2 * e]), r8 = ob4(r[2 * e + 1]), rs = rg >> 8, rs8 = r8 >> 8;
+                        const uint32_t x0 = u4_lo(rg), x1 = u4_lo(r8), x2 = u4_hi(rg), x3 = u4_hi(r8);
+                        const uint32_t y0 = u4_lo(rs), y1 = u4_lo(rs8), y2 = u4_hi(rs), y3 = u4_hi(rs8);
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr) {
+                            float d[4];
+                            mma16816_c(d, x0, x1, x2, x3, qh[nr][4 * mm], qh[nr][4 * mm + 1], nb[nr][2 * mm], nb[nr][2 * mm + 1]);
+                            mma16816(d, y0, y1, y2, y3, qh[nr][4 * mm + 2], qh[nr][4 * mm + 3]);
+                            if constexpr (LO) {
+                                mma16816(d, x0, x1, x2, x3, ql[nr][4 * mm], ql[nr][4 * mm + 1]);
+                                mma16816(d, y0, y1, y2, y3, ql[nr][4 * mm + 2], ql[nr][4 * mm + 3]);
+                            }
+                            a0[nr] = fma2(s0[2 * e], s0[2 * e + 1], d[0], d[1], a0[nr]);
+                            a1[nr] = fma2(s1[2 * e], s1[2 * e + 1], d[2], d[3], a1[nr]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e2 = 0; e2 < 2; ++e2) {
+                        uint32_t r[4];
+                        ldsm_x4(plane_at(kb, ko, kx, PK::R, tr, 4 * p + 2 * e2), r);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int mm = 4 * p + 2 * e2 + e;
+                            const uint32_t rg = ob8(r[2 * e]), r8 = ob8(r[2 * e + 1]);
+                            const uint32_t x0 = u8_lo(rg), x1 = u8_lo(r8), x2 = u8_lo(rg >> 8), x3 = u8_lo(r8 >> 8);
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr) {
+                                float d[4];
+                                mma16816_c(d, x0, x1, x2, x3, qh[nr][2 * mm], qh[nr][2 * mm + 1], nb[nr][mm], 0.f);
+                                if constexpr (LO) mma16816(d, x0, x1, x2, x3, ql[nr][2 * mm], ql[nr][2 * mm + 1]);
+                                a0[nr].x = fmaf(s0[2 * e2 + e], d[0], a0[nr].x);
+                                a1[nr].x = fmaf(s1[2 * e2 + e], d[2], a1[nr].x);
+                            }
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+                sc[nr][tt][0] = a0[nr].x + a0[nr].y;
+                sc[nr][tt][1] = a1[nr].x + a1[nr].y;
+            }
+        }
+        // ---- mask, online softmax ----
+        // (rows past the last have q~ = 0 and no output: they need no mask)
+        const bool edge = t0 + CH - 1 > pos_lo || (P.window && t0 < pos_hi - P.window + 1);
+        uint32_t pb[NR][NT][2];  // fp16 scales: (p of token g, p of token g + 8)
+        float pf[NR][NT][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            if (edge) {
+#pragma unroll
+                for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int t = t0 + 16 * tt + g + 8 * r;
+                        if (t > pos[nr] || t < low[nr]) sc[nr][tt][r] = -INFINITY;
+                    }
+            }
+            float mt = -INFINITY;
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt) mt = fmaxf(mt, fmaxf(sc[nr][tt][0], sc[nr][tt][1]));
+            mt *= kSub;
+            if (__any_sync(0xffffffffu, mt > mx[nr])) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+                const float mn = fmaxf(mx[nr], mt);
+                const float f = mn == -INFINITY ? 1.f : ex2(mx[nr] - mn);
+                l[nr] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) acc[nr][i] *= f;
+                mx[nr] = mn;
+            }
+            const float bias = mx[nr] == -INFINITY ? 0.f : mx[nr] - PBITS;
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt) {
+                pf[nr][tt][0] = ex2(fmaf(sc[nr][tt][0], kSub, -bias));
+                pf[nr][tt][1] = ex2(fmaf(sc[nr][tt][1], kSub, -bias));
+                l[nr] += pf[nr][tt][0] + pf[nr][tt][1];
+                if constexpr (SF == SRFTKV_SCALE_FP16) pb[nr][tt][0] = split::h2(pf[nr][tt][0], pf[nr][tt][1]);
+            }
+        }
+        // ---- acc += codes_V^T . (p scale) ----
+        const int hd = g >> 1, side = g & 1;
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt) {
+            const int tr = 16 * tt;
+            uint32_t q2[NR][2];  // fp16 scales: p of tokens (2c, 2c+1), (2c+8, 2c+9) of row hd
+            float p4[NR][4];     // otherwise: of tokens 2c, 2c+1, 2c+8, 2c+9
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+                if constexpr (SF == SRFTKV_SCALE_FP16) {
+                    const uint32_t u = __shfl_sync(0xffffffffu, pb[nr][tt][0], 8 * c + hd);
+                    const uint32_t w = __shfl_sync(0xffffffffu, pb[nr][tt][0], 8 * c + 4 + hd);
+                    q2[nr][0] = __byte_perm(u, w, 0x5410);
+                    q2[nr][1] = __byte_perm(u, w, 0x7632);
+                    if (BV == 8 && side) q2[nr][0] = q2[nr][1] = 0u;
+                } else {
+                    p4[nr][0] = __shfl_sync(0xffffffffu, pf[nr][tt][0], 8 * c + hd);
+                    p4[nr][1] = __shfl_sync(0xffffffffu, pf[nr][tt][0], 8 * c + 4 + hd);
+                    p4[nr][2] = __shfl_sync(0xffffffffu, pf[nr][tt][1], 8 * c + hd);
+                    p4[nr][3] = __shfl_sync(0xffffffffu, pf[nr][tt][1], 8 * c + 4 + hd);
+                    if (BV == 8 && side) p4[nr][0] = p4[nr][1] = p4[nr][2] = p4[nr][3] = 0.f;
+                }
+            }
+            const int t4[4] = {tr + 2 * c, tr + 2 * c + 1, tr + 2 * c + 8, tr + 2 * c + 9};
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                // units of this thread's column in the piece: 4-bit 2e + side (e = 0, 1), 8-bit all four
+                constexpr int NU = BV == 4 ? 2 : 4;
+                uint32_t s2[NU][2];
+                float sf[NU][4];
+                if constexpr (SF == SRFTKV_SCALE_FP16) {
+                    uint2 w[4];
+                    if (P.lg_group == 4) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint2*>(vs + (t4[k] * ng + 4 * p) * 2);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint16_t* row = reinterpret_cast<const uint16_t*>(vs) + t4[k] * ng;
+                            uint32_t v[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i] = row[(16 * (4 * p + i)) >> P.lg_group];
+                            w[k] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < NU; ++u) {
+                        const bool second = BV == 4 ? u == 1 : u >= 2;
+                        const uint32_t sel = (BV == 4 ? side : (u & 1)) ? 0x7632u : 0x5410u;
+                        s2[u][0] = __byte_perm(second ? w[0].y : w[0].x, second ? w[1].y : w[1].x, sel);
+                        s2[u][1] = __byte_perm(second ? w[2].y : w[2].x, second ? w[3].y : w[3].x, sel);
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < NU; ++u)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            sf[u][k] = split::scale_at<SF>(vs, t4[k], 4 * p + (BV == 4 ? 2 * u + side : u), ng, P.lg_group);
+                }
+                auto operand = [&](int nr, int u, uint32_t& b0, uint32_t& b1) {
+                    if constexpr (SF == SRFTKV_SCALE_FP16) {
+                        b0 = split::hmul2(q2[nr][0], s2[u][0]);
+                        b1 = split::hmul2(q2[nr][1], s2[u][1]);
+                    } else {
+                        const float2 f0 = mul2(p4[nr][0], p4[nr][1], sf[u][0], sf[u][1]);
+                        const float2 f1 = mul2(p4[nr][2], p4[nr][3], sf[u][2], sf[u][3]);
+                        b0 = split::h2(f0.x, f0.y);
+                        b1 = split::h2(f1.x, f1.y);
+                    }
+                };
+                if constexpr (BV == 4) {
+                    uint32_t r[4];
+                    ldsm_x4_t(plane_at(vb, vo, vx, PV::R, tr, 2 * p), r);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t R0 = ob4(r[2 * e]), R1 = ob4(r[2 * e + 1]), S0 = R0 >> 8, S1 = R1 >> 8;
+                        const uint32_t x0 = u4_lo(R0), x1 = u4_hi(R0), x2 = u4_lo(R1), x3 = u4_hi(R1);
+                        const uint32_t y0 = u4_lo(S0), y1 = u4_hi(S0), y2 = u4_lo(S1), y3 = u4_hi(S1);
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr) {
+                            uint32_t b0, b1;
+                            operand(nr, e, b0, b1);
+                            float(&f0)[4] = *reinterpret_cast<float(*)[4]>(&acc[nr][8 * (2 * p + e)]);
+                            float(&f1)[4] = *reinterpret_cast<float(*)[4]>(&acc[nr][8 * (2 * p + e) + 4]);
+                            mma16816(f0, x0, x1, x2, x3, b0, b1);
+                            mma16816(f1, y0, y1, y2, y3, b0, b1);
+                            // -8 in the units of the low (2^-24) and high (2^-20) nibbles
+                            mma16816(f0, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
+                            mma16816(f1, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e2 = 0; e2 < 2; ++e2) {
+                        uint32_t r[4];
+                        ldsm_x4_t(plane_at(vb, vo, vx, PV::R, tr, 4 * p + 2 * e2), r);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t R0 = ob8(r[2 * e]), R1 = ob8(r[2 * e + 1]);
+                            const uint32_t x0 = u8_lo(R0), x1 = u8_lo(R0 >> 8), x2 = u8_lo(R1), x3 = u8_lo(R1 >> 8);
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr) {
+                                uint32_t b0, b1;
+                                operand(nr, 2 * e2 + e, b0, b1);
+                                float(&f0)[4] = *reinterpret_cast<float(*)[4]>(&acc[nr][4 * (4 * p + 2 * e2 + e)]);
+                                mma16816(f0, x0, x1, x2, x3, b0, b1);
+                                mma16816(f0, 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, b0, b1);  // -128
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+    griddep_launch_dependents();
+    if (failed) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            mx[nr] = -INFINITY;
+            l[nr] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) acc[nr][i] = 0.f;
+        }
+    }
+
+    // ---- the four warps meet ----
+    if (__syncthreads_or(undrained ? 1 : 0)) {  // a copy that never landed keeps everybody out of the ring
+        for (int r = threadIdx.x; r < n_rows; r += blockDim.x)
+            if (W.n_parts > 1) {
+                float* ml = W.part_ml + (row_at(r) * W.n_parts + spl) * 2;
+                ml[0] = -INFINITY;
+                ml[1] = 0.f;
+            }
+        return;
+    }
+    float* mw = reinterpret_cast<float*>(smem);        // [warps][rows][2]
+    float* aw = mw + split::WARPS * M::ROWS * 2;       // [warps][rows][D]
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[nr] += __shfl_xor_sync(0xffffffffu, l[nr], off);
+        if (g == 0) {
+            mw[(warp * M::ROWS + 4 * nr + c) * 2] = mx[nr];
+            mw[(warp * M::ROWS + 4 * nr + c) * 2 + 1] = l[nr];
+        }
+        float* a = aw + (warp * M::ROWS + 4 * nr + c) * D;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) {
+            const int e = i & 3;
+            if constexpr (BV == 4) {  // rows g: dim 4g + 2j of the chunk (low nibbles), rows g + 8: the next one
+                const int cb = i >> 3, j = (i >> 2) & 1;
+                if ((e & 1) == (g >= 4 ? 1 : 0)) a[32 * cb + 4 * g + 2 * j + (e >> 1)] = acc[nr][i] * ((e >> 1) ? 1048576.f : kSub);
+            } else {
+                if ((e & 1) == 0) a[16 * (i >> 2) + 2 * g + (e >> 1)] = acc[nr][i] * kSub;
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int r = warp; r < n_rows; r += split::WARPS) {
+        float Mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < split::WARPS; ++w) Mx = fmaxf(Mx, mw[(w * M::ROWS + r) * 2]);
+        float L = 0.f, o[E] = {};
+        if (Mx != -INFINITY) {
+#pragma unroll
+            for (int w = 0; w < split::WARPS; ++w) {
+                const float f = ex2(mw[(w * M::ROWS + r) * 2] - Mx);
+                L = fmaf(f, mw[(w * M::ROWS + r) * 2 + 1], L);
+#pragma unroll
+                for (int j = 0; j < E; ++j) o[j] = fmaf(f, aw[(w * M::ROWS + r) * D + E * lane + j], o[j]);
+            }
+        }
+        if (W.n_parts > 1) {
+            const long long at = row_at(r) * W.n_parts + spl;
+            if (lane == 0) *reinterpret_cast<float2*>(W.part_ml + 2 * at) = make_float2(Mx, L);
+            float* a = W.part_acc + at * D + E * lane;
+            if constexpr (E == 2) *reinterpret_cast<float2*>(a) = make_float2(o[0], o[1]);
+            else {
+#pragma unroll
+                for (int j = 0; j < E / 4; ++j)
+                    reinterpret_cast<float4*>(a)[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+        } else {
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+            for (int j = 0; j < E; ++j) o[j] *= inv;
+            if (P.lam_v) {
+                float lam[E];
+                rot::load_lambda<D>(P.lam_v + (long long)h * D, lane, lam);
+#pragma unroll
+                for (int j = 0; j < E; ++j) o[j] = __fdiv_rn(o[j], lam[j]);
+            }
+            rot::inverse<D>(o, lane, P.tr_v, P.sign_mask, scratch);
+            uint16_t* dst = static_cast<uint16_t*>(P.out) + row_ptr(P.out, P.out_stride, r);
+            if (W.dtype == SRFTKV_DTYPE_BF16) rot::store_row<D>(reinterpret_cast<__nv_bfloat16*>(dst), lane, o);
+            else rot::store_row<D>(reinterpret_cast<__half*>(dst), lane, o);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+// The code plane [n_pages * H][page_size][row bytes]; a box is `rows` tokens of up to 128 bytes of their rows
+static bool encode_pages(CUtensorMap* map, const uint8_t* base, int rb, int page_size, long long ph, int rows) {
+    const unsigned long long dims[3] = {(unsigned long long)rb, (unsigned long long)page_size, (unsigned long long)ph};
+    const unsigned long long strides[2] = {(unsigned long long)rb, (unsigned long long)rb * page_size};
+    const int w = rb < 128 ? rb : 128;
+    const unsigned box[3] = {(unsigned)w, (unsigned)rows, 1u};
+    return encode_tiled_swz(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box,
+                            w == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                            : w == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      : CU_TENSOR_MAP_SWIZZLE_128B,
+                            "page codes");
+}
+
+template <int D, int BK, int BV, int SF, int NR>
+static int launch_split_one(const PagedAttnParams& P, const SplitWork& W, cudaStream_t stream) {
+    using C = split::Cfg<D, BK, BV, SF>;
+    using M = split::Smem<D, BK, BV, SF, NR>;
+    static_assert(M::BYTES <= 232448, "shared memory");
+    CUtensorMap tk, tv;
+    const int ps = 1 << P.lg_page, rows = C::CH < ps ? C::CH : ps;
+    if (!encode_pages(&tk, P.kc, C::RK, ps, (long long)P.n_pages * P.Hkv, rows) ||
+        !encode_pages(&tv, P.vc, C::RV, ps, (long long)P.n_pages * P.Hkv, rows))
+        return SRFTKV_ERR_CUDA;
+    SplitWork w = W;
+    w.chunks = W.tokens / C::CH;
+    auto* kernel = paged_attn_split_kernel<D, BK, BV, SF, NR>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, M::BYTES);
+    if (e == cudaSuccess) {
+        kernel<<<dim3(W.n_splits, P.B * P.Hkv, W.groups), 128, M::BYTES, stream>>>(tk, tv, P, w);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) {
+        set_error("paged attention launch failed: %s", cudaGetErrorString(e));
+        return SRFTKV_ERR_CUDA;
+    }
+    return SRFTKV_OK;
+}
+
+template <int D, int SF, int NR>
+static int launch_split_bits(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s) {
+    if (W.bits_k == 4) return W.bits_v == 4 ? launch_split_one<D, 4, 4, SF, NR>(P, W, s) : launch_split_one<D, 4, 8, SF, NR>(P, W, s);
+    return W.bits_v == 4 ? launch_split_one<D, 8, 4, SF, NR>(P, W, s) : launch_split_one<D, 8, 8, SF, NR>(P, W, s);
+}
+template <int D, int SF>
+static int launch_split(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s) {
+    if constexpr (D <= 128) {
+        if (W.nr == 2) return launch_split_bits<D, SF, 2>(P, W, s);
+    }
+    return launch_split_bits<D, SF, 1>(P, W, s);
+}
+
+}  // namespace srftkv

@@ -1,0 +1,8 @@
+// paged_attn_split128_e8m0.cu -- the paged attention's split kernel at d = 128 with e8m0 scales.
+#include "paged_attn_split.cuh"
+
+namespace srftkv {
+int launch_split128_e8m0(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s) {
+    return launch_split<128, SRFTKV_SCALE_E8M0>(P, W, s);
+}
+}  // namespace srftkv
