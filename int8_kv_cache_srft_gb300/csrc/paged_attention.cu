@@ -87,9 +87,15 @@ static Plan make_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q, int
         long long see = max_len;
         if (window) see = std::min<long long>(see, (long long)window + max_q - 1 + 31);
         const long long base = (long long)B * Hkv * p.S.groups;
-        long long s = (16 * sms + base - 1) / base;
-        s = std::max(1ll, std::min(s, (see + 255) / 256));
-        long long tokens = ((see + s - 1) / s + 127) / 128 * 128;
+        // two or three CTAs run on an SM: the split count that shortens waves * (tokens a split + its fixed part, the
+        // rotation, fragments and join, worth about 256 tokens of one CTA)
+        const long long at_once = (d == 256 || p.S.nr == 2 ? 2 : 3) * sms, fixed = 256;
+        long long tokens = 0, best_cost = -1;
+        for (long long s = 1; s <= std::min<long long>((see + 127) / 128, 256); ++s) {
+            const long long t = ((see + s - 1) / s + 127) / 128 * 128, n = (see + t - 1) / t;
+            const long long cost = (base * n + at_once - 1) / at_once * (t + fixed);
+            if (best_cost < 0 || cost < best_cost) tokens = t, best_cost = cost;
+        }
         p.S.tokens = (int)tokens;
         p.S.n_splits = (int)((see + tokens - 1) / tokens);
         p.n_parts = p.S.n_parts = p.S.n_splits;

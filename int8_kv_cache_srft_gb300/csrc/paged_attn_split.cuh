@@ -4,9 +4,16 @@
 // Grid (splits, sequence and kv head, row groups).  A CTA's 4 NR query rows
 // (query tokens times the heads of its kv head) share every byte it reads.
 // Each of its four warps streams every fourth chunk of CH tokens of the split
-// into its own ring of shared-memory stages (a swizzled TMA box a page for the
-// codes, a plain bulk copy for the scales, NS stages) and keeps its own online
-// softmax; the warps meet in shared memory at the end.
+// into its own ring of NS shared-memory stages and keeps its own online softmax;
+// the warps meet in shared memory at the end.  The copies are 16 bytes a lane
+// (cp.async): every lane finds its own page, rows past the end and pages that do
+// not exist arrive as zeros, and a chunk costs about 30 instructions.  TMA boxes
+// of 16 to 32 rows cost twice that in address and barrier work of one lane while
+// the others waited (515 against 447 us at 16 x 131072 tokens, d = 128, int4, fp16
+// scales), and one producer lane for four warps could not keep up (680 us).
+// Measured there: 6.0 TB/s with fp16 scales, 6.4 with fp32 (88 and 95 % of the
+// copy rate), 273 warp instructions a 16-token tile, issue slots 56 % busy; two
+// stages and four CTAs an SM 469 us, two and three 456, four and two 508.
 //
 //   S = codes_K . q~  with mma.sync m16n8k16: codes as exact fp16 (offset-binary
 //       subnormals, attn_frag.cuh), 16 tokens a tile; columns 2c, 2c+1 carry
@@ -28,7 +35,7 @@
 // below 65504 keeps p scale_V finite, and small scales above fp16's subnormals.
 #pragma once
 
-#include <cstring>
+#include <type_traits>
 
 #include "attn_frag.cuh"
 #include "paged.h"
@@ -45,8 +52,8 @@ template <int SF>
 constexpr int sbytes() { return SF == SRFTKV_SCALE_FP32 ? 4 : SF == SRFTKV_SCALE_FP16 ? 2 : 1; }
 constexpr int up(int v, int a) { return (v + a - 1) / a * a; }
 
-// A plane of code rows in shared memory: rows of up to 128 bytes, swizzled by TMA with the mode of their length;
-// 256-byte rows as two 128-byte halves one after the other
+// A plane of code rows in shared memory: rows of up to 128 bytes whose 16-byte pieces are XORed with their 128-byte
+// line (ldmatrix then reads without bank conflicts); 256-byte rows as two 128-byte halves one after the other
 template <int RB, int CH>
 struct Plane {
     static constexpr int R = RB < 128 ? RB : 128, HALVES = RB / R, BYTES = CH * RB;
@@ -59,9 +66,9 @@ struct Cfg {
     static constexpr int OFF_V = up(CH * RK, 1024), OFF_KS = OFF_V + up(CH * RV, 1024);
     static constexpr int OFF_VS = OFF_KS + up(CH * SR, 128);
     static constexpr int STAGE = up(OFF_VS + CH * SR, 1024);
-    static constexpr int NS = WARPS * 3 * STAGE <= 74 * 1024 ? 3 : 2;
+    static constexpr int NS = WARPS * 3 * STAGE <= 70 * 1024 ? 3 : 2;                       // stages a warp
 };
-template <int D, int BK, int BV, int SF, int NR>
+template <int D, int BK, int BV, int SF, int NR, bool LO>
 struct Smem {
     using C = Cfg<D, BK, BV, SF>;
     static constexpr int ROWS = 4 * NR;
@@ -69,44 +76,97 @@ struct Smem {
     static constexpr int MERGE = WARPS * ROWS * (D + 2) * 4;      // over the ring, at the end
     static constexpr int BODY = up(RING > MERGE ? RING : MERGE, 16);
     static constexpr int OFF_Q = BODY;                            // q~ rows
-    static constexpr int OFF_ROT = OFF_Q + ROWS * D * 4;          // a warp's rotation scratch
-    static constexpr int OFF_BAR = OFF_ROT + WARPS * D * 4;
-    static constexpr int BYTES = OFF_BAR + WARPS * C::NS * 16 + 1024;
+    static constexpr int OFF_QL = OFF_Q + ROWS * D * 4;           // the low halves of q~'s fragments (LO)
+    static constexpr int OFF_ROT = OFF_QL + (LO ? D / 32 * 512 : 0);  // a warp's rotation scratch
+    static constexpr int OFF_END = OFF_ROT + WARPS * D * 4;
+    static constexpr int BYTES = OFF_END + 1024;
 };
 
-// scale f (16-dim unit) of staged row r; ng: scales a row
-template <int SF>
-__device__ __forceinline__ float scale_at(const uint8_t* s, int r, int f, int ng, int lg) {
-    const int i = r * ng + (lg == 4 ? f : (16 * f) >> lg);
+// scale f (16-dim unit) of staged row r, rows of D/16 scales
+template <int D, int SF>
+__device__ __forceinline__ float scale_at(const uint8_t* s, int r, int f) {
+    const int i = r * (D / 16) + f;
     if constexpr (SF == SRFTKV_SCALE_FP32) return reinterpret_cast<const float*>(s)[i];
     else if constexpr (SF == SRFTKV_SCALE_FP16) return __half2float(reinterpret_cast<const __half*>(s)[i]);
     else return __uint_as_float((uint32_t)s[i] << 23);
 }
 // scales of units 4p .. 4p+3 of staged row r
-template <int SF>
-__device__ __forceinline__ void scales4(const uint8_t* s, int r, int p, int ng, int lg, float (&v)[4]) {
-    if (lg == 4) {
-        if constexpr (SF == SRFTKV_SCALE_FP32) {
-            const float4 f = *reinterpret_cast<const float4*>(s + (r * ng + 4 * p) * 4);
-            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-        } else if constexpr (SF == SRFTKV_SCALE_FP16) {
-            const uint2 w = *reinterpret_cast<const uint2*>(s + (r * ng + 4 * p) * 2);
-            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-            v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-        } else {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(s + r * ng + 4 * p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
-        }
+template <int D, int SF>
+__device__ __forceinline__ void scales4(const uint8_t* s, int r, int p, float (&v)[4]) {
+    const int i = r * (D / 16) + 4 * p;
+    if constexpr (SF == SRFTKV_SCALE_FP32) {
+        const float4 f = *reinterpret_cast<const float4*>(s + i * 4);
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else if constexpr (SF == SRFTKV_SCALE_FP16) {
+        const uint2 w = *reinterpret_cast<const uint2*>(s + i * 2);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
     } else {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(s + i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = scale_at<SF>(s, r, 4 * p + i, ng, lg);
+        for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(((w >> (8 * k)) & 0xFFu) << 23);
     }
+}
+// Groups wider than 16: spread the staged rows of D >> lg scales to rows of D/16 in place (lane r takes row r), so
+// the tiles are read with constant offsets whatever the group
+template <int D, int SF>
+__device__ __forceinline__ void spread_scales(uint8_t* s, int rows, int lg, int lane) {
+    using U = typename std::conditional<SF == SRFTKV_SCALE_FP32, uint32_t,
+                                        typename std::conditional<SF == SRFTKV_SCALE_FP16, uint16_t, uint8_t>::type>::type;
+    U* v = reinterpret_cast<U*>(s);
+    U t[D / 16];
+    if (lane < rows) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) t[i] = v[lane * (D >> lg) + ((16 * i) >> lg)];
+    }
+    __syncwarp();
+    if (lane < rows) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) v[lane * (D / 16) + i] = t[i];
+    }
+}
+// (w & mask) ^ flip as one logic op: the mask comes in a register the compiler cannot see through (two immediates
+// would take two)
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float opaque(float v) {
+    float r;
+    asm volatile("mov.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+template <uint32_t FLIP>
+__device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(mask), "n"(FLIP));  // (a & b) ^ c
+    return r;
 }
 __device__ __forceinline__ uint32_t h2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 16 bytes to shared memory, the first n of them from global memory and zeros behind them
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// D = A . B, m16n8k16
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// D = A . B + (c[0] .. c[3]), m16n8k16
+__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1, const float* c) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -116,16 +176,14 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 
 }  // namespace split
 
-template <int D, int BK, int BV, int SF, int NR>
+template <int D, int BK, int BV, int SF, int NR, bool LO>
 __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
-    paged_attn_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                            const __grid_constant__ PagedAttnParams P, const __grid_constant__ SplitWork W) {
+    paged_attn_split_kernel(const __grid_constant__ PagedAttnParams P, const __grid_constant__ SplitWork W) {
     using C = split::Cfg<D, BK, BV, SF>;
-    using M = split::Smem<D, BK, BV, SF, NR>;
+    using M = split::Smem<D, BK, BV, SF, NR, LO>;
     using PK = split::Plane<C::RK, C::CH>;
     using PV = split::Plane<C::RV, C::CH>;
     constexpr int CH = C::CH, NT = CH / 16, NS = C::NS, NP = D / 64, E = D / 32;
-    constexpr bool LO = NR == 1 && D <= 128;
     constexpr float PBITS = BV == 4 ? 2.f : 6.f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -168,55 +226,63 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
         return;
     }
 
-    // ---- the ring: barriers and bad-page masks of this warp's stages ----
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::OFF_BAR) + warp * NS;
-    uint32_t* bad = reinterpret_cast<uint32_t*>(smem + M::OFF_BAR + split::WARPS * NS * 8) + warp * NS;
+    // ---- copies of a chunk into a stage of this warp's ring, 16 bytes a lane and step ----
     uint8_t* ring = smem + warp * NS * C::STAGE;
-    if (lane == 0) {
-        for (int s = 0; s < NS; ++s) ptx::mbar_init(ptx::smem_u32(&bars[s]), 1);
-        ptx::fence_barrier_init();
-    }
-    __syncwarp();
-    const int ng = D >> P.lg_group, srb = ng * split::sbytes<SF>();
-    const int box = min(CH, 1 << P.lg_page), boxes = CH / box;  // tokens of a chunk that lie in one page
+    const int srb = (D >> P.lg_group) * split::sbytes<SF>();  // staged scale row as it lies in the page
     const int* table = P.table + (long long)b * P.max_pages;
-    const int psize = 1 << P.lg_page;
-    // one lane's copies of a chunk into stage s: the pages that hold its tokens below len
-    auto issue = [&](int chunk, int s) {
-        const uint32_t bar = ptx::smem_u32(&bars[s]);
-        uint8_t* st = ring + s * C::STAGE;
-        const int t0 = chunk * CH, n_box = min(boxes, (len - t0 + box - 1) / box);
-        ptx::mbar_arrive_expect_tx(bar, n_box * box * (C::RK + C::RV + 2 * srb));
-        uint32_t mask = 0;
-        for (int x = 0; x < n_box; ++x) {
-            const int t = t0 + x * box;
-            int pg = __ldg(table + (t >> P.lg_page));
-            if ((unsigned)pg >= (unsigned)P.n_pages) {
-                mask |= 1u << x;
-                pg = 0;
-                atomicOr(P.fault, kFaultPage);
-            }
-            const int ph = pg * P.Hkv + h, off = t & (psize - 1);
-            const long long row = (long long)ph * psize + off;
+    int pages[NT];  // of the next chunk to load, looked up a chunk ahead
+    auto look_up = [&](int chunk) {
 #pragma unroll
-            for (int hv = 0; hv < PK::HALVES; ++hv)
-                ptx::tma_load_3d(ptx::smem_u32(st + hv * (CH * 128) + x * box * PK::R), &tm_k, bar, hv * 128, off, ph);
-#pragma unroll
-            for (int hv = 0; hv < PV::HALVES; ++hv)
-                ptx::tma_load_3d(ptx::smem_u32(st + C::OFF_V + hv * (CH * 128) + x * box * PV::R), &tm_v, bar, hv * 128, off, ph);
-            ptx::bulk_load(ptx::smem_u32(st + C::OFF_KS + x * box * srb), P.ks + row * srb, box * srb, bar);
-            ptx::bulk_load(ptx::smem_u32(st + C::OFF_VS + x * box * srb), P.vs + row * srb, box * srb, bar);
+        for (int x = 0; x < NT; ++x) {
+            const int t = chunk * CH + 16 * x;
+            pages[x] = chunk < c_end && t < len ? __ldg(table + (t >> P.lg_page)) : 0;
         }
-        bad[s] = mask;
     };
-    // bad[] is written after the arrival here, so a stage's mask is ordered for the other lanes by the __syncwarp
-    // that follows every issue
-    if (lane == 0) {
+    auto load = [&](int chunk, int s) {
+        if (chunk < c_end) {
+            const uint32_t st = ptx::smem_u32(ring + s * C::STAGE);
+            const int t0 = chunk * CH;
+            long long row[NT];  // packed row of token 16 x of the chunk
+            int have[NT];       // tokens of the 16 that are there
 #pragma unroll
-        for (int j = 0; j < NS - 1; ++j)
-            if (c_begin + warp + j * split::WARPS < c_end) issue(c_begin + warp + j * split::WARPS, j);
-    }
-    __syncwarp();
+            for (int x = 0; x < NT; ++x) {
+                const bool ok = (unsigned)pages[x] < (unsigned)P.n_pages;
+                have[x] = ok ? len - t0 - 16 * x : 0;
+                if (!ok) atomicOr(P.fault, kFaultPage);
+                row[x] = ok ? (long long)(pages[x] * P.Hkv + h) << P.lg_page | ((t0 + 16 * x) & ((1 << P.lg_page) - 1)) : 0;
+            }
+            auto codes = [&](const uint8_t* plane, uint32_t dst, auto pl, auto rbc) {
+                using PL = decltype(pl);
+                constexpr int RB = decltype(rbc)::value, LPR = RB / 16, RPI = 32 / LPR, PER = PL::R / 16;
+                const int lr = lane / LPR, col = lane % LPR;
+#pragma unroll
+                for (int i = 0; i < CH / RPI; ++i) {
+                    const int x = i * RPI / 16, r = i * RPI + lr;
+                    split::copy16(dst + (col / PER) * (CH * 128) + r * PL::R + (((col % PER) ^ PL::swz(r)) << 4),
+                                  plane + (row[x] + (r & 15)) * RB + col * 16, (r & 15) < have[x] ? 16 : 0);
+                }
+            };
+            codes(P.kc, st, PK{}, std::integral_constant<int, C::RK>{});
+            codes(P.vc, st + C::OFF_V, PV{}, std::integral_constant<int, C::RV>{});
+            // scales: the 16 rows of a half lie one after the other, 16 srb bytes
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int j = 0; j < (C::SR + 31) / 32; ++j) {
+                    const int at = (32 * j + lane) * 16;  // byte of the half's scales
+                    if (at < 16 * srb) {
+                        const int n = min(max(have[x] * srb - at, 0), 16);
+                        split::copy16(st + C::OFF_KS + 16 * x * srb + at, P.ks + row[x] * srb + (n ? at : 0), n);
+                        split::copy16(st + C::OFF_VS + 16 * x * srb + at, P.vs + row[x] * srb + (n ? at : 0), n);
+                    }
+                }
+            look_up(chunk + split::WARPS);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up(c_begin + warp);
+#pragma unroll
+    for (int j = 0; j < NS - 1; ++j) load(c_begin + warp + j * split::WARPS, j);
 
     // ---- q~ = R q sm_scale log2 e / lambda_K, one warp a row ----
     float* qs = reinterpret_cast<float*>(smem + M::OFF_Q);
@@ -243,10 +309,13 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
     }
     __syncthreads();
 
-    // ---- K-side B fragments: column g = (row g/2, half g%2); nb: the accumulator's start, minus the code offset
-    // times the column sum, for this thread's columns 2c, 2c+1 ----
-    constexpr int NB = D / 16;
-    uint32_t qh[NR][D / 8], ql[LO ? NR : 1][LO ? D / 8 : 1];
+    // ---- K-side B fragments: column g = (row g/2, half g%2); nb: minus the code offset times the column sum, for
+    // this thread's columns 2c, 2c+1: the accumulators' start where registers allow to keep whole ones (QUAD; built
+    // anew they cost four moves a tile and chunk), else added times the scale ----
+    constexpr bool QUAD = BK == 4 && NR == 1 && !LO && D <= 128;  // nb kept as whole accumulator starts
+    constexpr int NB = QUAD ? D / 8 : D / 16;
+    uint32_t qh[NR][D / 8];
+    uint4* qlo = reinterpret_cast<uint4*>(smem + M::OFF_QL);  // [D/32][lane]: every warp's are the same
     float nb[NR][NB];
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
@@ -260,21 +329,29 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
                 const float4 e = *reinterpret_cast<const float4*>(q + 32 * mm + 8 * c + 4);
                 const float x[4] = {a.x * on, a.y * on, a.z * on, a.w * on}, y[4] = {e.x * on, e.y * on, e.z * on, e.w * on};
                 float part = 0.f;
+                uint32_t ql[4] = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float u = (j & 1) ? 0.0625f : 1.f;
                     if constexpr (LO) {
-                        split_h2(x[j] * u, y[j] * u, qh[nr][4 * mm + j], ql[nr][4 * mm + j]);
-                        part += (h2_sum(qh[nr][4 * mm + j]) + h2_sum(ql[nr][4 * mm + j])) * ((j & 1) ? 16.f : 1.f);
+                        split_h2(x[j] * u, y[j] * u, qh[nr][4 * mm + j], ql[j]);
+                        part += (h2_sum(qh[nr][4 * mm + j]) + h2_sum(ql[j])) * ((j & 1) ? 16.f : 1.f);
                     } else {
                         qh[nr][4 * mm + j] = split::h2(x[j] * u, y[j] * u);
                         part += h2_sum(qh[nr][4 * mm + j]) * ((j & 1) ? 16.f : 1.f);
                     }
                 }
+                if (LO && warp == 0) qlo[mm * 32 + lane] = make_uint4(ql[0], ql[1], ql[2], ql[3]);
                 part += __shfl_xor_sync(0xffffffffu, part, 1);
                 part += __shfl_xor_sync(0xffffffffu, part, 2);
-                nb[nr][2 * mm] = (-8.f / kSub) * __shfl_sync(0xffffffffu, part, 8 * c);
-                nb[nr][2 * mm + 1] = (-8.f / kSub) * __shfl_sync(0xffffffffu, part, 8 * c + 4);
+                const float n0 = (-8.f / kSub) * __shfl_sync(0xffffffffu, part, 8 * c);
+                const float n1 = (-8.f / kSub) * __shfl_sync(0xffffffffu, part, 8 * c + 4);
+                if constexpr (QUAD) {
+                    nb[nr][4 * mm] = split::opaque(n0), nb[nr][4 * mm + 1] = split::opaque(n1);
+                    nb[nr][4 * mm + 2] = split::opaque(n0), nb[nr][4 * mm + 3] = split::opaque(n1);
+                } else {
+                    nb[nr][2 * mm] = n0, nb[nr][2 * mm + 1] = n1;
+                }
             }
         } else {
             const float on = (g & 1) ? 0.f : 1.f;
@@ -283,9 +360,11 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
                 const float4 a = *reinterpret_cast<const float4*>(q + 16 * mm + 4 * c);
                 float part;
                 if constexpr (LO) {
-                    split_h2(a.x * on, a.z * on, qh[nr][2 * mm], ql[nr][2 * mm]);
-                    split_h2(a.y * on, a.w * on, qh[nr][2 * mm + 1], ql[nr][2 * mm + 1]);
-                    part = h2_sum(qh[nr][2 * mm]) + h2_sum(ql[nr][2 * mm]) + h2_sum(qh[nr][2 * mm + 1]) + h2_sum(ql[nr][2 * mm + 1]);
+                    uint32_t l0, l1;
+                    split_h2(a.x * on, a.z * on, qh[nr][2 * mm], l0);
+                    split_h2(a.y * on, a.w * on, qh[nr][2 * mm + 1], l1);
+                    if (warp == 0) reinterpret_cast<uint2*>(qlo + (mm >> 1) * 32 + lane)[mm & 1] = make_uint2(l0, l1);
+                    part = h2_sum(qh[nr][2 * mm]) + h2_sum(l0) + h2_sum(qh[nr][2 * mm + 1]) + h2_sum(l1);
                 } else {
                     qh[nr][2 * mm] = split::h2(a.x * on, a.z * on);
                     qh[nr][2 * mm + 1] = split::h2(a.y * on, a.w * on);
@@ -297,6 +376,8 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
             }
         }
     }
+
+    if constexpr (LO) __syncthreads();  // qlo
 
     float acc[NR][D / 4], mx[NR], l[NR];
     int pos[NR], low[NR];  // row c of each group: the last and first position it sees
@@ -319,42 +400,29 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
         return base + (seg / per) * (CH * 128) + off + tr * R + (((uint32_t)(seg % per) << 4) ^ x16);
     };
 
-    bool failed = false, undrained = false;
+    // codes -> offset-binary fp16 subnormals (attn_frag.cuh)
+    const uint32_t m_lo = split::opaque(0x000F000Fu), m_hi = split::opaque(0x00F000F0u), m_by = split::opaque(0x00FF00FFu);
+    // the V side's offset as an A operand: -8 in the units of low (2^-24) and high (2^-20) nibbles, or -128 of bytes;
+    // four registers kept as they are (as immediates they were moved into place before every use)
+    const uint32_t off0 = split::opaque(BV == 4 ? 0x80088008u : 0x80808080u), off1 = split::opaque(0x80808080u);
+    const uint32_t off2 = split::opaque(BV == 4 ? 0x80088008u : 0x80808080u), off3 = split::opaque(0x80808080u);
+    auto lo4 = [&](uint32_t w) { return split::pick<0x00080008u>(w, m_lo); };
+    auto hi4 = [&](uint32_t w) { return split::pick<0x00800080u>(w, m_hi); };
+    auto by8 = [&](uint32_t w) { return split::pick<0x00800080u>(w, m_by); };
+
     int it = 0;
     for (int chunk = c_begin + warp; chunk < c_end; chunk += split::WARPS, ++it) {
-        const int s = it % NS, nxt = chunk + (NS - 1) * split::WARPS;
-        if (lane == 0 && nxt < c_end) issue(nxt, (it + NS - 1) % NS);
-        __syncwarp();
-        if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(ptx::smem_u32(&bars[s]), (it / NS) & 1))) {
-            if (lane == 0) {
-                atomicOr(P.fault, kFaultWait);
-                bool all = true;  // this warp's copies in flight land before its shared memory is used for anything else
-                for (int j = 0; j < NS; ++j)
-                    if (chunk + j * split::WARPS < c_end)
-                        all &= ptx::mbar_wait_bounded(ptx::smem_u32(&bars[(it + j) % NS]), ((it + j) / NS) & 1, 1u << 16);
-                undrained = !all;
-            }
-            undrained = __shfl_sync(0xffffffffu, undrained, 0);
-            failed = true;
-            break;
-        }
+        const int s = it % NS;
+        asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+        __syncwarp();  // the chunk is there for every lane, and the stage before it is free
+        load(chunk + (NS - 1) * split::WARPS, (it + NS - 1) % NS);
         uint8_t* st = ring + s * C::STAGE;
         const uint32_t kb = ptx::smem_u32(st), vb = ptx::smem_u32(st + C::OFF_V);
         uint8_t *ks = st + C::OFF_KS, *vs = st + C::OFF_VS;
-        const int t0 = chunk * CH, have = len - t0;
-        const uint32_t bad_mask = bad[s];
-        if (have < CH || bad_mask) {
-            // rows past the end may hold anything: their scales become zeros (p is zero there, and zero times
-            // anything but a NaN or an infinity); so do a bad page's rows, K and V
-            for (int r = lane; r < CH; r += 32) {
-                const bool gone = (bad_mask >> (r / box)) & 1;
-                if (r >= have || gone)
-                    for (int k = 0; k < srb; ++k) {
-                        vs[r * srb + k] = 0;
-                        ks[r * srb + k] = 0;
-                    }
-            }
-            ptx::fence_proxy_async_smem();
+        const int t0 = chunk * CH;
+        if (P.lg_group != 4) {
+            split::spread_scales<D, SF>(ks, CH, P.lg_group, lane);
+            split::spread_scales<D, SF>(vs, CH, P.lg_group, lane);
             __syncwarp();
         }
         // ---- scores: sc[nr][st][r] of row c, token 16 st + g + 8 r, in units of 2^-24 ----
@@ -368,28 +436,36 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 float s0[4], s1[4];
-                split::scales4<SF>(ks, tr + g, p, ng, P.lg_group, s0);
-                split::scales4<SF>(ks, tr + g + 8, p, ng, P.lg_group, s1);
+                split::scales4<D, SF>(ks, tr + g, p, s0);
+                split::scales4<D, SF>(ks, tr + g + 8, p, s1);
                 if constexpr (BK == 4) {
                     uint32_t r[4];
                     ldsm_x4(plane_at(kb, ko, kx, PK::R, tr, 2 * p), r);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int mm = 2 * p + e;
-                        const uint32_t rg = ob4(r[2 * e]), r8 = ob4(r[2 * e + 1]), rs = rg >> 8, rs8 = r8 >> 8;
-                        const uint32_t x0 = u4_lo(rg), x1 = u4_lo(r8), x2 = u4_hi(rg), x3 = u4_hi(r8);
-                        const uint32_t y0 = u4_lo(rs), y1 = u4_lo(rs8), y2 = u4_hi(rs), y3 = u4_hi(rs8);
+                        const uint32_t rg = r[2 * e], r8 = r[2 * e + 1], rs = rg >> 8, rs8 = r8 >> 8;
+                        const uint32_t x0 = lo4(rg), x1 = lo4(r8), x2 = hi4(rg), x3 = hi4(r8);
+                        const uint32_t y0 = lo4(rs), y1 = lo4(rs8), y2 = hi4(rs), y3 = hi4(rs8);
 #pragma unroll
                         for (int nr = 0; nr < NR; ++nr) {
                             float d[4];
-                            mma16816_c(d, x0, x1, x2, x3, qh[nr][4 * mm], qh[nr][4 * mm + 1], nb[nr][2 * mm], nb[nr][2 * mm + 1]);
+                            if constexpr (QUAD)
+                                split::mma16816_from(d, x0, x1, x2, x3, qh[nr][4 * mm], qh[nr][4 * mm + 1], &nb[nr][4 * mm]);
+                            else
+                                split::mma16816_zero(d, x0, x1, x2, x3, qh[nr][4 * mm], qh[nr][4 * mm + 1]);
                             mma16816(d, y0, y1, y2, y3, qh[nr][4 * mm + 2], qh[nr][4 * mm + 3]);
                             if constexpr (LO) {
-                                mma16816(d, x0, x1, x2, x3, ql[nr][4 * mm], ql[nr][4 * mm + 1]);
-                                mma16816(d, y0, y1, y2, y3, ql[nr][4 * mm + 2], ql[nr][4 * mm + 3]);
+                                const uint4 q4 = qlo[mm * 32 + lane];
+                                mma16816(d, x0, x1, x2, x3, q4.x, q4.y);
+                                mma16816(d, y0, y1, y2, y3, q4.z, q4.w);
                             }
                             a0[nr] = fma2(s0[2 * e], s0[2 * e + 1], d[0], d[1], a0[nr]);
                             a1[nr] = fma2(s1[2 * e], s1[2 * e + 1], d[2], d[3], a1[nr]);
+                            if constexpr (!QUAD) {
+                                a0[nr] = fma2(s0[2 * e], s0[2 * e + 1], nb[nr][2 * mm], nb[nr][2 * mm + 1], a0[nr]);
+                                a1[nr] = fma2(s1[2 * e], s1[2 * e + 1], nb[nr][2 * mm], nb[nr][2 * mm + 1], a1[nr]);
+                            }
                         }
                     }
                 } else {
@@ -397,18 +473,20 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
                     for (int e2 = 0; e2 < 2; ++e2) {
                         uint32_t r[4];
                         ldsm_x4(plane_at(kb, ko, kx, PK::R, tr, 4 * p + 2 * e2), r);
+                        uint4 q4;
+                        if constexpr (LO) q4 = qlo[(2 * p + e2) * 32 + lane];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int mm = 4 * p + 2 * e2 + e;
-                            const uint32_t rg = ob8(r[2 * e]), r8 = ob8(r[2 * e + 1]);
-                            const uint32_t x0 = u8_lo(rg), x1 = u8_lo(r8), x2 = u8_lo(rg >> 8), x3 = u8_lo(r8 >> 8);
+                            const uint32_t rg = r[2 * e], r8 = r[2 * e + 1];
+                            const uint32_t x0 = by8(rg), x1 = by8(r8), x2 = by8(rg >> 8), x3 = by8(r8 >> 8);
 #pragma unroll
                             for (int nr = 0; nr < NR; ++nr) {
                                 float d[4];
-                                mma16816_c(d, x0, x1, x2, x3, qh[nr][2 * mm], qh[nr][2 * mm + 1], nb[nr][mm], 0.f);
-                                if constexpr (LO) mma16816(d, x0, x1, x2, x3, ql[nr][2 * mm], ql[nr][2 * mm + 1]);
-                                a0[nr].x = fmaf(s0[2 * e2 + e], d[0], a0[nr].x);
-                                a1[nr].x = fmaf(s1[2 * e2 + e], d[2], a1[nr].x);
+                                split::mma16816_zero(d, x0, x1, x2, x3, qh[nr][2 * mm], qh[nr][2 * mm + 1]);
+                                if constexpr (LO) mma16816(d, x0, x1, x2, x3, e ? q4.z : q4.x, e ? q4.w : q4.y);
+                                a0[nr].x = fmaf(s0[2 * e2 + e], d[0] + nb[nr][mm], a0[nr].x);
+                                a1[nr].x = fmaf(s1[2 * e2 + e], d[2] + nb[nr][mm], a1[nr].x);
                             }
                         }
                     }
@@ -491,19 +569,8 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
                 float sf[NU][4];
                 if constexpr (SF == SRFTKV_SCALE_FP16) {
                     uint2 w[4];
-                    if (P.lg_group == 4) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint2*>(vs + (t4[k] * ng + 4 * p) * 2);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint16_t* row = reinterpret_cast<const uint16_t*>(vs) + t4[k] * ng;
-                            uint32_t v[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[i] = row[(16 * (4 * p + i)) >> P.lg_group];
-                            w[k] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-                        }
-                    }
+                    for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint2*>(vs + (t4[k] * (D / 16) + 4 * p) * 2);
 #pragma unroll
                     for (int u = 0; u < NU; ++u) {
                         const bool second = BV == 4 ? u == 1 : u >= 2;
@@ -516,7 +583,7 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
                     for (int u = 0; u < NU; ++u)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            sf[u][k] = split::scale_at<SF>(vs, t4[k], 4 * p + (BV == 4 ? 2 * u + side : u), ng, P.lg_group);
+                            sf[u][k] = split::scale_at<D, SF>(vs, t4[k], 4 * p + (BV == 4 ? 2 * u + side : u));
                 }
                 auto operand = [&](int nr, int u, uint32_t& b0, uint32_t& b1) {
                     if constexpr (SF == SRFTKV_SCALE_FP16) {
@@ -534,9 +601,9 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
                     ldsm_x4_t(plane_at(vb, vo, vx, PV::R, tr, 2 * p), r);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t R0 = ob4(r[2 * e]), R1 = ob4(r[2 * e + 1]), S0 = R0 >> 8, S1 = R1 >> 8;
-                        const uint32_t x0 = u4_lo(R0), x1 = u4_hi(R0), x2 = u4_lo(R1), x3 = u4_hi(R1);
-                        const uint32_t y0 = u4_lo(S0), y1 = u4_hi(S0), y2 = u4_lo(S1), y3 = u4_hi(S1);
+                        const uint32_t R0 = r[2 * e], R1 = r[2 * e + 1], S0 = R0 >> 8, S1 = R1 >> 8;
+                        const uint32_t x0 = lo4(R0), x1 = hi4(R0), x2 = lo4(R1), x3 = hi4(R1);
+                        const uint32_t y0 = lo4(S0), y1 = hi4(S0), y2 = lo4(S1), y3 = hi4(S1);
 #pragma unroll
                         for (int nr = 0; nr < NR; ++nr) {
                             uint32_t b0, b1;
@@ -545,9 +612,8 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
                             float(&f1)[4] = *reinterpret_cast<float(*)[4]>(&acc[nr][8 * (2 * p + e) + 4]);
                             mma16816(f0, x0, x1, x2, x3, b0, b1);
                             mma16816(f1, y0, y1, y2, y3, b0, b1);
-                            // -8 in the units of the low (2^-24) and high (2^-20) nibbles
-                            mma16816(f0, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
-                            mma16816(f1, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
+                            mma16816(f0, off0, off1, off2, off3, b0, b1);
+                            mma16816(f1, off0, off1, off2, off3, b0, b1);
                         }
                     }
                 } else {
@@ -557,44 +623,26 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
                         ldsm_x4_t(plane_at(vb, vo, vx, PV::R, tr, 4 * p + 2 * e2), r);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const uint32_t R0 = ob8(r[2 * e]), R1 = ob8(r[2 * e + 1]);
-                            const uint32_t x0 = u8_lo(R0), x1 = u8_lo(R0 >> 8), x2 = u8_lo(R1), x3 = u8_lo(R1 >> 8);
+                            const uint32_t R0 = r[2 * e], R1 = r[2 * e + 1];
+                            const uint32_t x0 = by8(R0), x1 = by8(R0 >> 8), x2 = by8(R1), x3 = by8(R1 >> 8);
 #pragma unroll
                             for (int nr = 0; nr < NR; ++nr) {
                                 uint32_t b0, b1;
                                 operand(nr, 2 * e2 + e, b0, b1);
                                 float(&f0)[4] = *reinterpret_cast<float(*)[4]>(&acc[nr][4 * (4 * p + 2 * e2 + e)]);
                                 mma16816(f0, x0, x1, x2, x3, b0, b1);
-                                mma16816(f0, 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, b0, b1);  // -128
+                                mma16816(f0, off0, off1, off2, off3, b0, b1);
                             }
                         }
                     }
                 }
             }
         }
-        __syncwarp();
     }
     griddep_launch_dependents();
-    if (failed) {
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            mx[nr] = -INFINITY;
-            l[nr] = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 4; ++i) acc[nr][i] = 0.f;
-        }
-    }
 
-    // ---- the four warps meet ----
-    if (__syncthreads_or(undrained ? 1 : 0)) {  // a copy that never landed keeps everybody out of the ring
-        for (int r = threadIdx.x; r < n_rows; r += blockDim.x)
-            if (W.n_parts > 1) {
-                float* ml = W.part_ml + (row_at(r) * W.n_parts + spl) * 2;
-                ml[0] = -INFINITY;
-                ml[1] = 0.f;
-            }
-        return;
-    }
+    // ---- the four warps meet, over the ring (its copies have all been waited for: the last groups are empty) ----
+    __syncthreads();
     float* mw = reinterpret_cast<float*>(smem);        // [warps][rows][2]
     float* aw = mw + split::WARPS * M::ROWS * 2;       // [warps][rows][D]
 #pragma unroll
@@ -664,35 +712,17 @@ __global__ void __launch_bounds__(128, D == 256 || NR == 2 ? 2 : 3)
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// The code plane [n_pages * H][page_size][row bytes]; a box is `rows` tokens of up to 128 bytes of their rows
-static bool encode_pages(CUtensorMap* map, const uint8_t* base, int rb, int page_size, long long ph, int rows) {
-    const unsigned long long dims[3] = {(unsigned long long)rb, (unsigned long long)page_size, (unsigned long long)ph};
-    const unsigned long long strides[2] = {(unsigned long long)rb, (unsigned long long)rb * page_size};
-    const int w = rb < 128 ? rb : 128;
-    const unsigned box[3] = {(unsigned)w, (unsigned)rows, 1u};
-    return encode_tiled_swz(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box,
-                            w == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
-                            : w == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                      : CU_TENSOR_MAP_SWIZZLE_128B,
-                            "page codes");
-}
-
-template <int D, int BK, int BV, int SF, int NR>
+template <int D, int BK, int BV, int SF, int NR, bool LO>
 static int launch_split_one(const PagedAttnParams& P, const SplitWork& W, cudaStream_t stream) {
     using C = split::Cfg<D, BK, BV, SF>;
-    using M = split::Smem<D, BK, BV, SF, NR>;
+    using M = split::Smem<D, BK, BV, SF, NR, LO>;
     static_assert(M::BYTES <= 232448, "shared memory");
-    CUtensorMap tk, tv;
-    const int ps = 1 << P.lg_page, rows = C::CH < ps ? C::CH : ps;
-    if (!encode_pages(&tk, P.kc, C::RK, ps, (long long)P.n_pages * P.Hkv, rows) ||
-        !encode_pages(&tv, P.vc, C::RV, ps, (long long)P.n_pages * P.Hkv, rows))
-        return SRFTKV_ERR_CUDA;
     SplitWork w = W;
     w.chunks = W.tokens / C::CH;
-    auto* kernel = paged_attn_split_kernel<D, BK, BV, SF, NR>;
+    auto* kernel = paged_attn_split_kernel<D, BK, BV, SF, NR, LO>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, M::BYTES);
     if (e == cudaSuccess) {
-        kernel<<<dim3(W.n_splits, P.B * P.Hkv, W.groups), 128, M::BYTES, stream>>>(tk, tv, P, w);
+        kernel<<<dim3(W.n_splits, P.B * P.Hkv, W.groups), 128, M::BYTES, stream>>>(P, w);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) {
@@ -702,17 +732,21 @@ static int launch_split_one(const PagedAttnParams& P, const SplitWork& W, cudaSt
     return SRFTKV_OK;
 }
 
-template <int D, int SF, int NR>
+template <int D, int SF, int NR, bool LO>
 static int launch_split_bits(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s) {
-    if (W.bits_k == 4) return W.bits_v == 4 ? launch_split_one<D, 4, 4, SF, NR>(P, W, s) : launch_split_one<D, 4, 8, SF, NR>(P, W, s);
-    return W.bits_v == 4 ? launch_split_one<D, 8, 4, SF, NR>(P, W, s) : launch_split_one<D, 8, 8, SF, NR>(P, W, s);
+    if (W.bits_k == 4)
+        return W.bits_v == 4 ? launch_split_one<D, 4, 4, SF, NR, LO>(P, W, s) : launch_split_one<D, 4, 8, SF, NR, LO>(P, W, s);
+    return W.bits_v == 4 ? launch_split_one<D, 8, 4, SF, NR, LO>(P, W, s) : launch_split_one<D, 8, 8, SF, NR, LO>(P, W, s);
 }
+// LO: bf16 rows carry 8 bits and their answer is rounded to 8, so q~ in fp16 alone (11) is not what limits it; fp16
+// rows get hi + lo where registers allow (6 % of the time at 16 x 131072 tokens)
 template <int D, int SF>
 static int launch_split(const PagedAttnParams& P, const SplitWork& W, cudaStream_t s) {
     if constexpr (D <= 128) {
-        if (W.nr == 2) return launch_split_bits<D, SF, 2>(P, W, s);
+        if (W.nr == 2) return launch_split_bits<D, SF, 2, false>(P, W, s);
+        if (W.dtype == SRFTKV_DTYPE_FP16) return launch_split_bits<D, SF, 1, true>(P, W, s);
     }
-    return launch_split_bits<D, SF, 1>(P, W, s);
+    return launch_split_bits<D, SF, 1, false>(P, W, s);
 }
 
 }  // namespace srftkv
