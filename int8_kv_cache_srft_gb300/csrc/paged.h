@@ -28,6 +28,8 @@ struct PagedCodecParams {
     int n_sides;
     const int64_t* slots;
     int n_tokens, H, group, lg_group, lg_page;
+    uint32_t div_mul;     // division by H as a multiply and a shift (make_fastdiv)
+    int div_shift;
     long long n_slots;    // n_pages * page_size
     unsigned int* fault;
     uint32_t sign_mask[128];
@@ -39,6 +41,10 @@ struct PagedCodecCall {
     int d, dtype;
     cudaStream_t stream;
 };
+// Many rows on the tensor cores (paged_codec_tc.cuh); both sides of P share the transform
+int launch_paged_codec_tc64(const PagedCodecParams& P, int dtype, bool write, cudaStream_t s);
+int launch_paged_codec_tc128(const PagedCodecParams& P, int dtype, bool write, cudaStream_t s);
+int launch_paged_codec_tc256(const PagedCodecParams& P, int dtype, bool write, cudaStream_t s);
 int paged_quantize(const PagedCodecCall& c);
 int paged_dequantize(const PagedCodecCall& c);
 unsigned int paged_codec_take_fault();

@@ -142,16 +142,11 @@ __global__ void __launch_bounds__(PW * 32) paged_dequantize_warp_kernel(const __
 }
 
 template <int D, typename T>
-static int launch_warp(const PagedCodecCall& c, bool quantize) {
-    PagedCodecParams P = c.P;
-    static SymbolCache cache;
-    void* f = nullptr;
-    if (symbol_address(cache, &g_paged_codec_fault, &f, "the paged codec's fault word")) return SRFTKV_ERR_CUDA;
-    P.fault = static_cast<unsigned int*>(f);
+static int launch_warp(const PagedCodecParams& P, cudaStream_t stream, bool quantize) {
     const long long rows = (long long)P.n_tokens * P.H * P.n_sides;
     const unsigned blocks = (unsigned)((rows + PW - 1) / PW);
-    if (quantize) paged_quantize_warp_kernel<D, T><<<blocks, PW * 32, 0, c.stream>>>(P);
-    else paged_dequantize_warp_kernel<D, T><<<blocks, PW * 32, 0, c.stream>>>(P);
+    if (quantize) paged_quantize_warp_kernel<D, T><<<blocks, PW * 32, 0, stream>>>(P);
+    else paged_dequantize_warp_kernel<D, T><<<blocks, PW * 32, 0, stream>>>(P);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
         set_error("paged codec launch failed: %s", cudaGetErrorString(e));
@@ -159,16 +154,35 @@ static int launch_warp(const PagedCodecCall& c, bool quantize) {
     }
     return SRFTKV_OK;
 }
-
 template <int D>
-static int launch_d(const PagedCodecCall& c, bool quantize) {
-    return c.dtype == SRFTKV_DTYPE_BF16 ? launch_warp<D, __nv_bfloat16>(c, quantize) : launch_warp<D, __half>(c, quantize);
+static int launch_d(const PagedCodecParams& P, int dtype, cudaStream_t stream, bool quantize) {
+    return dtype == SRFTKV_DTYPE_BF16 ? launch_warp<D, __nv_bfloat16>(P, stream, quantize)
+                                      : launch_warp<D, __half>(P, stream, quantize);
 }
 
 static int launch(const PagedCodecCall& c, bool quantize) {
-    if (c.d == 64) return launch_d<64>(c, quantize);
-    if (c.d == 128) return launch_d<128>(c, quantize);
-    return launch_d<256>(c, quantize);
+    PagedCodecParams P = c.P;
+    static SymbolCache cache;
+    void* f = nullptr;
+    if (symbol_address(cache, &g_paged_codec_fault, &f, "the paged codec's fault word")) return SRFTKV_ERR_CUDA;
+    P.fault = static_cast<unsigned int*>(f);
+    const FastDiv div = make_fastdiv((uint32_t)P.H);
+    P.div_mul = div.mul;
+    P.div_shift = div.shift;
+    // Many rows: the tensor cores, which every CTA first builds R_s for (10 us a call at d = 128, 6 at 64, 19 to 30 at
+    // 256); few: one warp a row (d = 128: 8.8 us at 8192 rows, 14.3 at 16384; d = 64: 5.9 and 9.4; d = 256: 20 and 36
+    // at 16384 and 32768).  The write's epilogue holds 32 columns a thread, so its groups end there; both sides rotate
+    // with one R_s.
+    const long long rows = (long long)P.n_tokens * P.H * P.n_sides;
+    const bool one_r = P.n_sides == 1 || P.side[0].transform == P.side[1].transform;
+    if (rows >= (c.d == 256 ? 20480 : 10240) && one_r && (!quantize || P.group <= 32)) {
+        if (c.d == 64) return launch_paged_codec_tc64(P, c.dtype, quantize, c.stream);
+        if (c.d == 128) return launch_paged_codec_tc128(P, c.dtype, quantize, c.stream);
+        return launch_paged_codec_tc256(P, c.dtype, quantize, c.stream);
+    }
+    if (c.d == 64) return launch_d<64>(P, c.dtype, c.stream, quantize);
+    if (c.d == 128) return launch_d<128>(P, c.dtype, c.stream, quantize);
+    return launch_d<256>(P, c.dtype, c.stream, quantize);
 }
 int paged_quantize(const PagedCodecCall& c) { return launch(c, true); }
 int paged_dequantize(const PagedCodecCall& c) { return launch(c, false); }
