@@ -33,6 +33,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "codec_tc_common.cuh"
 #include "paged.h"
 #include "ptx.cuh"
@@ -73,20 +75,30 @@ struct Cfg {
     static_assert(SMEM <= 232448, "shared memory");
 };
 
-// B operand stored MN-major (rows of the contraction index, 64 of N a 128-byte row): 8-row groups 1024 bytes
-// apart, 64-column blocks `lbo` bytes apart, 128-byte swizzle
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(lbo >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
+// Descriptors as two words, so that a loop steps through an operand by adding to the low one.  K-major, 128-byte
+// swizzle (tc::sw128_desc); and MN-major (rows of the contraction index, 64 of N a 128-byte row): 8-row groups 1024
+// bytes apart, 64-column blocks `lbo` bytes apart.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
+// One thread of a converged warp.  The MMA warp runs its loop as a whole and only the issue is one thread's: with the
+// loop itself in one thread every operand was moved to a uniform register at its use, and eight MMAs took 900 cycles to
+// issue that take 512 to run.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
     return tc::idesc_f16_f32(M, N) | (b_mn ? 1u << 16 : 0u);
 }
+
+// A softmax thread holds a row of P (64 registers) beside two loads of S (32); a dequantising one needs half of that.
+// The kernel is compiled for kRegs a thread (launch_tile checks it): 8 warps give back 16, 8 take them (at 64 the others spilled).
+constexpr int kRegs = 96;
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 112;"); }
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, relative error about 2^-22
     float y;
@@ -379,19 +391,21 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
         }
         ptx::fence_proxy_async_smem();
         __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int i = 0; i < n_qt; ++i)
-#pragma unroll 1
+        if (warp == 0 && tile::elect()) {
+            const uint32_t bo = tile::desc_k(sbase + C::OFF_K);
+            for (int i = 0; i < n_qt; ++i) {
+                const uint32_t ao = tile::desc_k(sbase + i * C::QB), dst = tmem + C::R_COL + i * 128 + nh * NB;
+#pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint64_t ad = tc::sw128_desc(sbase + i * C::QB + (ks >> 2) * 16384 + (ks & 3) * 32);
-                    const uint32_t bo = sbase + C::OFF_K + (ks >> 2) * (NB * 128) + (ks & 3) * 32;
-                    const uint32_t dst = tmem + C::R_COL + i * 128 + nh * NB;
-                    tc::mma_f16(dst, ad, tc::sw128_desc(bo), tile::idesc(128, NB, false), ks > 0);
-                    tc::mma_f16(dst, ad, tc::sw128_desc(bo + NB * D * 2), tile::idesc(128, NB, false), 1);
+                    const uint32_t as = (ks >> 2) * 1024 + (ks & 3) * 2, bs = (ks >> 2) * (NB * 8) + (ks & 3) * 2;
+                    tc::mma_f16(dst, tile::desc(ao + as), tile::desc(bo + bs), tile::idesc(128, NB, false), ks > 0);
+                    tc::mma_f16(dst, tile::desc(ao + as), tile::desc(bo + bs + NB * D / 8), tile::idesc(128, NB, false), 1);
                 }
+            }
             tc::commit(bar(ROT));
         }
-        if (!ptx::mbar_wait_bounded(bar(ROT), nh & 1)) failed = true;
+        __syncwarp();
+        if (!ptx::mbar_spin_bounded(bar(ROT), nh & 1)) failed = true;
         tc::fence_after_sync();
         __syncthreads();
     }
@@ -427,21 +441,17 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
 
     const int n0 = dual ? (n + 1) / 2 : n;  // steps of stream 0
     auto steps_of = [&](int i) { return dual ? (n + 1 - i) / 2 : n; };
-    auto wait1 = [&](int which, uint32_t parity) -> bool {  // one thread
-        if (ptx::mbar_wait_bounded(bar(which), parity)) return true;
-        failed = true;
-        return false;
-    };
     auto wait = [&](int which, uint32_t parity) -> bool {  // a whole warp, converged afterwards
-        if (__all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar(which), parity))) return true;
+        if (__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(which), parity))) return true;
         failed = true;
         return false;
     };
 
-    if (!failed && warp >= SMW && warp < 8) {
-        // (d = 256: the second softmax group has nothing to do)
-    } else if (!failed && warp < SMW) {
+    // (d = 256: warps 4-7 have nothing to do)
+    if (warp < SMW) {
         // =========================== softmax ===========================
+        if (NQ == 2) tile::more_registers();
+        if (!failed) {
         const int i = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int r = (dual ? 0 : i * 128) + 32 * (warp & 3) + lane;
@@ -463,23 +473,40 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                 const uint32_t s_col = tmem + lanes + sb * C::S_STEP, p_col = tmem + lanes + C::P_COL + sb * C::P_STEP;
                 const int hi = pos - t0, lo = first - t0;  // visible columns lo .. hi
                 const bool full = __all_sync(0xffffffffu, hi >= BN - 1 && lo <= 0);
-                float mt = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < BN / 32; ++c) {
-                    uint32_t v[32];
-                    tc::ld_32x32b_x32(s_col + 32 * c, v);
-                    tc::wait_ld(v);
-                    if (!full) {
+                // One pass: P with the maximum in use so far, and the tile's own maximum beside it.  The former may lag
+                // by kLazy (P stays below 2^8); where a row of the warp outgrew that, O is rescaled and the pass
+                // is taken again, from S, which is still there: P stays in registers until the vote.
+                uint32_t p[BN / 2];
+                float sum = 0.f;
+                auto pass = [&](float mu) -> float {
+                    float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    float mt[2] = {-INFINITY, -INFINITY};
+                    uint32_t v[2][16];
+                    tc::ld_32x32b_x16(s_col, v[0]);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * c + e > hi || 32 * c + e < lo) v[e] = 0xFF800000u;
+                    for (int c = 0; c < BN / 16; ++c) {
+                        uint32_t(&w)[16] = v[c & 1];
+                        tc::wait_ld(w);
+                        if (c + 1 < BN / 16) tc::ld_32x32b_x16(s_col + 16 * (c + 1), v[(c + 1) & 1]);
+                        if (!full) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (16 * c + e > hi || 16 * c + e < lo) w[e] = 0xFF800000u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float a = __uint_as_float(w[2 * e]), d = __uint_as_float(w[2 * e + 1]);
+                            mt[e & 1] = fmaxf(mt[e & 1], fmaxf(a, d));
+                            const float2 x = __fadd2_rn(make_float2(a, d), make_float2(-mu, -mu));
+                            const float2 y = make_float2(tile::ex2(x.x), tile::ex2(x.y));
+                            s2[e & 1] = __fadd2_rn(s2[e & 1], y);
+                            p[8 * c + e] = pack_half2(y.x, y.y);
+                        }
                     }
-                    float a[4] = {mt, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) a[e & 3] = fmaxf(a[e & 3], __uint_as_float(v[e]));
-                    mt = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
-                }
-                // the maximum in use may lag behind the true one by kLazy
+                    sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+                    return fmaxf(mt[0], mt[1]);
+                };
+                const float mt = pass(mx == -INFINITY ? 0.f : mx);
                 const bool grow = mt > mx + tile::kLazy || (mx == -INFINITY && mt > -INFINITY);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float mn = fmaxf(mx, mt);
@@ -499,30 +526,11 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                             tc::st_32x32b_x32(o_col + 32 * c, v);
                         }
                     }
+                    pass(mx == -INFINITY ? 0.f : mx);
                 }
-                const float mu = mx == -INFINITY ? 0.f : mx;
-                float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                for (int c = 0; c < BN / 32; ++c) {
-                    uint32_t v[32], p[16];
-                    tc::ld_32x32b_x32(s_col + 32 * c, v);
-                    tc::wait_ld(v);
-                    if (!full) {
+                l += sum;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * c + e > hi || 32 * c + e < lo) v[e] = 0xFF800000u;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float a = tile::ex2(__uint_as_float(v[2 * e]) - mu);
-                        const float d = tile::ex2(__uint_as_float(v[2 * e + 1]) - mu);
-                        s4[(2 * e) & 3] += a;
-                        s4[(2 * e + 1) & 3] += d;
-                        p[e] = pack_half2(a, d);
-                    }
-                    tc::st_32x32b_x16(p_col + 16 * c, p);
-                }
-                l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                for (int c = 0; c < BN / 64; ++c) tc::st_32x32b_x32(p_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(p + 32 * c));
                 tc::wait_st();
                 tc::fence_before_sync();
             }
@@ -617,8 +625,11 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                 }
             }
         }
-    } else if (!failed && warp < 16) {
+        }
+    } else if (warp >= 8 && warp < 16) {
         // =========================== dequantise ===========================
+        if (NQ == 2) tile::fewer_registers();
+        if (!failed) {
         constexpr int DP = BN * D / 256;        // coordinates a thread
         constexpr int PER = D / DP;             // threads a row
         const int dt = threadIdx.x - 256, r = dt / PER, x0 = (dt % PER) * DP;
@@ -675,31 +686,37 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                 if (lane == 0) ptx::mbar_arrive(bar(R_FULL));
             }
         }
-    } else if (!failed && lane == 0) {
+        }
+    } else if (!failed && warp == 16) {
         // =========================== MMA ===========================
+        const bool one = tile::elect();
+        const uint32_t qd = tile::desc_k(sbase), kd = tile::desc_k(sbase + C::OFF_K),
+                       vd = tile::desc_mn(sbase + C::OFF_V, BN * 128);
         auto issue_s = [&](int sb, int qt, int t) {
-            const uint32_t kb = sbase + C::OFF_K + (t & 1) * C::TB;
+            const uint32_t ao = qd + qt * (C::QB / 16), bo = kd + (t & 1) * (C::TB / 16), dst = tmem + sb * C::S_STEP;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-                tc::mma_f16(tmem + sb * C::S_STEP, tc::sw128_desc(sbase + qt * C::QB + (ks >> 2) * 16384 + (ks & 3) * 32),
-                            tc::sw128_desc(kb + (ks >> 2) * (BN * 128) + (ks & 3) * 32), tile::idesc(128, BN, false), ks > 0);
+                tc::mma_f16(dst, tile::desc(ao + (ks >> 2) * 1024 + (ks & 3) * 2), tile::desc(bo + (ks >> 2) * (BN * 8) + (ks & 3) * 2),
+                            tile::idesc(128, BN, false), ks > 0);
         };
         auto issue_pv = [&](int sb, int oc, int t, bool first) {
-            const uint32_t vb = sbase + C::OFF_V + (t & 1) * C::TB;
+            const uint32_t bo = vd + (t & 1) * (C::TB / 16), dst = tmem + C::O_COL + oc, pa = tmem + C::P_COL + sb * C::P_STEP;
 #pragma unroll
             for (int ks = 0; ks < BN / 16; ++ks)
-                tc::mma_f16_ta(tmem + C::O_COL + oc, tmem + C::P_COL + sb * C::P_STEP + 8 * ks, tile::desc_mn(vb + ks * 2048, BN * 128),
-                               tile::idesc(128, D, true), !(first && ks == 0));
+                tc::mma_f16_ta(dst, pa + 8 * ks, tile::desc(bo + ks * 128), tile::idesc(128, D, true), !(first && ks == 0));
         };
         if constexpr (NQ == 2) {
             auto start_s = [&](int i, int j) -> bool {  // S of stream i, step j; false: a wait ran out
                 const int t = dual ? 2 * j + i : j;
                 if (t >= n) return true;
-                if ((i == 0 || dual) && !wait1(K_FULL + (t & 1), (t >> 1) & 1)) return false;
+                if ((i == 0 || dual) && !wait(K_FULL + (t & 1), (t >> 1) & 1)) return false;
                 tc::fence_after_sync();
-                issue_s(i, dual ? 0 : i, t);
-                if (i == 1 || dual) tc::commit(bar(K_EMPTY + (t & 1)));
-                tc::commit(bar(S_FULL + i));
+                if (one) {
+                    issue_s(i, dual ? 0 : i, t);
+                    if (i == 1 || dual) tc::commit(bar(K_EMPTY + (t & 1)));
+                    tc::commit(bar(S_FULL + i));
+                }
+                __syncwarp();
                 return true;
             };
             bool ok = start_s(0, 0) && start_s(1, 0);
@@ -707,43 +724,56 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                 for (int i = 0; ok && i < 2; ++i) {
                     const int t = dual ? 2 * j + i : j;
                     if (t >= n) continue;
-                    ok = (i == 1 && !dual || wait1(V_FULL + (t & 1), (t >> 1) & 1)) && wait1(P_FULL + i, j & 1);
+                    ok = ((i == 1 && !dual) || wait(V_FULL + (t & 1), (t >> 1) & 1)) && wait(P_FULL + i, j & 1);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    issue_pv(i, i * D, t, j == 0);
-                    tc::commit(bar(PV_DONE + i));
-                    if (i == 1 || dual) tc::commit(bar(V_EMPTY + (t & 1)));
+                    if (one) {
+                        issue_pv(i, i * D, t, j == 0);
+                        tc::commit(bar(PV_DONE + i));
+                        if (i == 1 || dual) tc::commit(bar(V_EMPTY + (t & 1)));
+                    }
+                    __syncwarp();
                     ok = start_s(i, j + 1);
                 }
         } else {
             auto start_s = [&](int t) -> bool {
                 if (t >= n) return true;
-                if (!wait1(K_FULL + (t & 1), (t >> 1) & 1)) return false;
+                if (!wait(K_FULL + (t & 1), (t >> 1) & 1)) return false;
                 tc::fence_after_sync();
-                issue_s(t & 1, 0, t);
-                tc::commit(bar(K_EMPTY + (t & 1)));
-                tc::commit(bar(S_FULL + (t & 1)));
+                if (one) {
+                    issue_s(t & 1, 0, t);
+                    tc::commit(bar(K_EMPTY + (t & 1)));
+                    tc::commit(bar(S_FULL + (t & 1)));
+                }
+                __syncwarp();
                 return true;
             };
             bool ok = start_s(0) && start_s(1);
             for (int t = 0; ok && t < n; ++t) {
-                ok = wait1(V_FULL + (t & 1), (t >> 1) & 1) && wait1(P_FULL + (t & 1), (t >> 1) & 1);
+                ok = wait(V_FULL + (t & 1), (t >> 1) & 1) && wait(P_FULL + (t & 1), (t >> 1) & 1);
                 if (!ok) break;
                 tc::fence_after_sync();
-                issue_pv(t & 1, 0, t, t == 0);
-                tc::commit(bar(PV_DONE));
-                tc::commit(bar(V_EMPTY + (t & 1)));
+                if (one) {
+                    issue_pv(t & 1, 0, t, t == 0);
+                    tc::commit(bar(PV_DONE));
+                    tc::commit(bar(V_EMPTY + (t & 1)));
+                }
+                __syncwarp();
                 ok = start_s(t + 2);
             }
         }
-        if (W.n_parts == 1 && !failed && wait1(R_FULL, 0) && wait1(EP_FULL, 0)) {
+        if (W.n_parts == 1 && !failed && wait(R_FULL, 0) && wait(EP_FULL, 0)) {
             tc::fence_after_sync();
-            for (int i = 0; i < NQ; ++i)
-#pragma unroll 1
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc::mma_f16(tmem + i * 128, tc::sw128_desc(sbase + i * C::QB + (ks >> 2) * 16384 + (ks & 3) * 32),
-                                tile::desc_mn(sbase + C::OFF_K + ks * 2048, D * 128), tile::idesc(128, D, true), ks > 0);
-            tc::commit(bar(OUT_FULL));
+            if (one) {
+                const uint32_t bo = tile::desc_mn(sbase + C::OFF_K, D * 128);
+                for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        tc::mma_f16(tmem + i * 128, tile::desc(qd + i * (C::QB / 16) + (ks >> 2) * 1024 + (ks & 3) * 2),
+                                    tile::desc(bo + ks * 128), tile::idesc(128, D, true), ks > 0);
+                tc::commit(bar(OUT_FULL));
+            }
+            __syncwarp();
         }
     }
     if (failed) atomicOr(P.fault, kFaultWait);
@@ -756,7 +786,20 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
 template <int D>
 static int launch_tile(const PagedAttnParams& P, const TileWork& W, int blocks, cudaStream_t stream) {
     using C = tile::Cfg<D>;
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    // the registers the warps pass to each other are counted on kRegs at launch: another count would leave some waiting
+    static std::atomic<int> regs{0};
+    cudaError_t e = cudaSuccess;
+    if (regs.load() == 0) {
+        cudaFuncAttributes at;
+        e = cudaFuncGetAttributes(&at, paged_attn_tile_kernel<D>);
+        if (e == cudaSuccess) regs.store(at.numRegs);
+    }
+    if (e == cudaSuccess && C::NQ == 2 && (regs.load() + 7) / 8 * 8 != tile::kRegs) {
+        set_error("paged attention: the tile kernel was built for %d registers a thread, not %d", regs.load(), tile::kRegs);
+        return SRFTKV_ERR_CUDA;
+    }
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(paged_attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e == cudaSuccess) {
         paged_attn_tile_kernel<D><<<dim3(P.B * P.Hkv, blocks, W.n_splits), tile::THREADS, C::SMEM, stream>>>(P, W);
         e = cudaGetLastError();

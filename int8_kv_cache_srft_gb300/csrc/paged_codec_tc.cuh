@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_quantize_tc_kernel(cons
         for (int j = 0; j < (C::AHEAD ? PD : 1); ++j) load(first + j * step, j);
         auto empty = [&](int tile) -> bool {  // the stage of this CTA's tile number `tile` has been read
             if (tile < C::ST) return true;
-            return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar(S::A_EMPTY + tile % C::ST), (tile / C::ST - 1) & 1));
+            return __all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(S::A_EMPTY + tile % C::ST), (tile / C::ST - 1) & 1));
         };
         int i_tile = 0;
         for (int u = first; u < total; u += step, ++i_tile) {
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_quantize_tc_kernel(cons
             const PagedSideK& sd = P.side[t.side];
             const int r = 32 * quarter + lane;
             const long long row = ctc::row_of(P, t.t0 + r, t.h);
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar(S::ACC_FULL + a), (i_tile / C::NACC) & 1))) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(S::ACC_FULL + a), (i_tile / C::NACC) & 1))) {
                 failed = true;
                 break;
             }
@@ -298,26 +298,30 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_quantize_tc_kernel(cons
                 __syncwarp();
             }
         }
-    } else if (lane == 0) {
+    } else {
+        const bool one = tile::elect();
         int i_tile = 0;
         for (int u = first; u < total; u += step, ++i_tile) {
             const int s = i_tile % C::ST, a = i_tile % C::NACC;
-            if (!ptx::mbar_wait_bounded(bar(S::A_FULL + s), (i_tile / C::ST) & 1) ||
-                (i_tile >= C::NACC && !ptx::mbar_wait_bounded(bar(S::ACC_EMPTY + a), (i_tile / C::NACC - 1) & 1))) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(S::A_FULL + s), (i_tile / C::ST) & 1)) ||
+                (i_tile >= C::NACC &&
+                 !__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(S::ACC_EMPTY + a), (i_tile / C::NACC - 1) & 1)))) {
                 failed = true;
                 break;
             }
             tc::fence_after_sync();
-            const uint32_t ab = sbase + C::OFF_A + s * C::A_BYTES;
+            if (one) {
+                const uint32_t ao = tile::desc_k(sbase + C::OFF_A + s * C::A_BYTES), bo = tile::desc_k(sbase), dst = tmem + a * C::NB;
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint64_t ad = tc::sw128_desc(ab + (ks >> 2) * 16384 + (ks & 3) * 32);
-                const uint32_t bo = sbase + (ks >> 2) * (C::NB * 128) + (ks & 3) * 32;
-                tc::mma_f16(tmem + a * C::NB, ad, tc::sw128_desc(bo), tile::idesc(128, C::NB, false), ks > 0);
-                tc::mma_f16(tmem + a * C::NB, ad, tc::sw128_desc(bo + C::NB * D * 2), tile::idesc(128, C::NB, false), 1);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t as = (ks >> 2) * 1024 + (ks & 3) * 2, bs = (ks >> 2) * (C::NB * 8) + (ks & 3) * 2;
+                    tc::mma_f16(dst, tile::desc(ao + as), tile::desc(bo + bs), tile::idesc(128, C::NB, false), ks > 0);
+                    tc::mma_f16(dst, tile::desc(ao + as), tile::desc(bo + bs + C::NB * D / 8), tile::idesc(128, C::NB, false), 1);
+                }
+                tc::commit(bar(S::A_EMPTY + s));
+                tc::commit(bar(S::ACC_FULL + a));
             }
-            tc::commit(bar(S::A_EMPTY + s));
-            tc::commit(bar(S::ACC_FULL + a));
+            __syncwarp();
         }
     }
     if (failed) atomicOr(P.fault, kFaultWait);
@@ -419,7 +423,7 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(co
                 load(u + PD * step, i_tile % PD, row);  // (the pieces are this thread's own: read before they are replaced)
                 row = row_of(u + (PD + 1) * step);
             }
-            if (use > 0 && !__all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar(S::A_EMPTY + s), (use - 1) & 1))) {
+            if (use > 0 && !__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(S::A_EMPTY + s), (use - 1) & 1))) {
                 failed = true;
                 break;
             }
@@ -472,7 +476,7 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(co
             // this lane's place in the coalesced stores: 16-byte piece lane % 4 of rows lane / 4 + 8 j
             uint16_t* x = static_cast<uint16_t*>(sd.x) + (long long)(t.t0 + 32 * quarter + (lane >> 2)) * sd.x_stride +
                           (long long)t.h * D + c0 + 8 * (lane & 3);
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar(S::ACC_FULL + a), (i_tile / C::NACC) & 1))) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(S::ACC_FULL + a), (i_tile / C::NACC) & 1))) {
                 failed = true;
                 break;
             }
@@ -512,23 +516,28 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(co
                 __syncwarp();
             }
         }
-    } else if (lane == 0) {
+    } else {
+        const bool one = tile::elect();
         int i_tile = 0;
         for (int u = first; u < total; u += step, ++i_tile) {
             const int s = i_tile % C::ST, a = i_tile % C::NACC;
-            if (!ptx::mbar_wait_bounded(bar(S::A_FULL + s), (i_tile / C::ST) & 1) ||
-                (i_tile >= C::NACC && !ptx::mbar_wait_bounded(bar(S::ACC_EMPTY + a), (i_tile / C::NACC - 1) & 1))) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(S::A_FULL + s), (i_tile / C::ST) & 1)) ||
+                (i_tile >= C::NACC &&
+                 !__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(S::ACC_EMPTY + a), (i_tile / C::NACC - 1) & 1)))) {
                 failed = true;
                 break;
             }
             tc::fence_after_sync();
-            const uint32_t ab = sbase + C::OFF_A + s * C::A_BYTES;
+            if (one) {
+                const uint32_t ao = tile::desc_k(sbase + C::OFF_A + s * C::A_BYTES), bo = tile::desc_mn(sbase, D * 128);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                tc::mma_f16(tmem + a * D, tc::sw128_desc(ab + (ks >> 2) * 16384 + (ks & 3) * 32),
-                            tile::desc_mn(sbase + ks * 2048, D * 128), tile::idesc(128, D, true), ks > 0);
-            tc::commit(bar(S::A_EMPTY + s));
-            tc::commit(bar(S::ACC_FULL + a));
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc::mma_f16(tmem + a * D, tile::desc(ao + (ks >> 2) * 1024 + (ks & 3) * 2), tile::desc(bo + ks * 128),
+                                tile::idesc(128, D, true), ks > 0);
+                tc::commit(bar(S::A_EMPTY + s));
+                tc::commit(bar(S::ACC_FULL + a));
+            }
+            __syncwarp();
         }
     }
     if (failed) atomicOr(P.fault, kFaultWait);
