@@ -78,6 +78,8 @@ struct TileWork {
     int tps;             // tiles a split
     int n_parts;         // partial results a row: n_splits * (dual ? 2 : 1); 1: the kernel writes `out` itself
     int bits_k, bits_v, dtype;
+    uint8_t* images;     // the tiles laid down as fp16, [B * Hkv][tiles][K, V], or null: turned where they are used
+    int tiles;           // tiles of max_len
     float* part_ml;      // [total_q * Hq][n_parts][2]: m (log2 units), l
     float* part_acc;     // [total_q * Hq][n_parts][D]
 };

@@ -72,9 +72,14 @@ struct Plan {
     TileWork W;
     int blocks;      // tile kernel: row blocks a (sequence, kv head)
     int n_parts;     // partial results a row; 1: written as the answer at once
-    size_t acc_off;  // part_ml at 0, part_acc here
+    bool expand;     // tile kernel: the tiles are laid down as fp16 first
+    size_t img_off;  // part_ml at 0, part_acc at acc_off, images here
+    size_t acc_off;
     size_t bytes;
 };
+// The most workspace that laying tiles down may take (an eighth of it is what one layer of 128 k tokens and 2 kv heads
+// takes); past it they are turned where they are used.
+constexpr size_t kMaxImages = 1ull << 30;
 static Plan make_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window) {
     Plan p = {};
     const int rep = Hq / Hkv;
@@ -126,6 +131,16 @@ static Plan make_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q, int
         const size_t n = (size_t)total_q * Hq * p.n_parts;
         p.acc_off = (n * 8 + 255) / 256 * 256;
         p.bytes = p.acc_off + n * d * 4;
+    }
+    if (!p.few && p.blocks >= 3) {
+        const int bn = d == 256 ? 64 : 128;
+        p.W.tiles = (max_len + bn - 1) / bn;
+        const size_t img = (size_t)B * Hkv * p.W.tiles * (4 * bn * d);
+        if (img <= kMaxImages) {
+            p.expand = true;
+            p.img_off = (p.bytes + 255) / 256 * 256;
+            p.bytes = p.img_off + img;
+        }
     }
     return p;
 }
@@ -180,6 +195,7 @@ int paged_attention(const PagedAttnCall& c) {
         W.dtype = c.dtype;
         W.part_ml = ml;
         W.part_acc = acc;
+        W.images = plan.expand ? static_cast<uint8_t*>(c.workspace) + plan.img_off : nullptr;
         rc = c.d == 64    ? launch_tile64(P, W, plan.blocks, c.stream)
              : c.d == 128 ? launch_tile128(P, W, plan.blocks, c.stream)
                           : launch_tile256(P, W, plan.blocks, c.stream);

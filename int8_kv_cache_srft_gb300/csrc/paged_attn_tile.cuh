@@ -21,6 +21,12 @@
 // other's P.V and next S run.  At d = 256 O takes half of tensor memory, so
 // one q tile alternates between two S buffers instead.
 //
+// Many blocks of rows read the same tiles, and turning codes into fp16 costs as
+// many instructions as the softmax: with three blocks or more a kernel before
+// this one lays every tile down once, as the image it has in shared memory
+// (paged_expand_kernel, into the workspace), and the tiles arrive by one bulk
+// copy each.
+//
 // Few rows (at most 128 a sequence and kv head, "dual"): both streams hold the
 // same rows and take every other tile, each with its own m, l and O, joined by
 // the combine kernel like splits of the cache.
@@ -35,6 +41,7 @@
 
 #include <atomic>
 
+#include "attn_frag.cuh"
 #include "codec_tc_common.cuh"
 #include "paged.h"
 #include "ptx.cuh"
@@ -99,12 +106,6 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
 constexpr int kRegs = 96;
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 112;"); }
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
-
-__device__ __forceinline__ float ex2(float x) {  // 2^x, relative error about 2^-22
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // 16-byte chunk (8 consecutive inputs x0..) of row n of R_s as fp16 hi (and lo)
 template <int D, bool LO>
@@ -263,6 +264,49 @@ __device__ __forceinline__ void store_piece_any(uint8_t* tile, int r, int x0, in
 
 }  // namespace tile
 
+// The tiles of one (sequence, kv head) as fp16 images: K then V, each TB bytes as the tile kernel wants it in shared
+// memory.  Tiles that no query sees are left out.
+template <int D>
+__global__ void __launch_bounds__(256) paged_expand_kernel(const __grid_constant__ PagedAttnParams P,
+                                                           const __grid_constant__ TileWork W) {
+    using C = tile::Cfg<D>;
+    constexpr int BN = C::BN, DP = BN * D / 256, PER = D / DP;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int t = blockIdx.x, b = blockIdx.y / P.Hkv, h = blockIdx.y - b * P.Hkv;
+    const int len = min(max(P.seq_lens[b], 0), P.max_len);
+    const int m_tok = P.cu_q ? min(max(P.cu_q[b + 1] - P.cu_q[b], 0), P.max_q) : 1;
+    const int low = P.window ? len - m_tok - P.window + 1 : 0;  // the first token the first query sees
+    if (t * BN < len && (t + 1) * BN > low) {
+        const int r = threadIdx.x / PER, x0 = (threadIdx.x % PER) * DP, tok = t * BN + r;
+        long long row = -1;
+        if (tok < len) {
+            const int pg = __ldg(P.table + (long long)b * P.max_pages + (tok >> P.lg_page));
+            if ((unsigned)pg < (unsigned)P.n_pages)
+                row = (((long long)pg * P.Hkv + h) << P.lg_page) | (tok & ((1 << P.lg_page) - 1));
+            else
+                atomicOr(P.fault, kFaultPage);
+        }
+        tile::Piece<DP> pk, pv;
+        tile::load_piece<D, DP>(P.kc, P.ks, row, x0, W.bits_k, P.sfmt, P.lg_group, pk);
+        tile::load_piece<D, DP>(P.vc, P.vs, row, x0, W.bits_v, P.sfmt, P.lg_group, pv);
+        const bool lo = P.sfmt == SRFTKV_SCALE_FP32;
+        tile::store_piece_any<D, BN, DP>(smem, r, x0, W.bits_k, lo, pk);
+        tile::store_piece_any<D, BN, DP>(smem + C::TB, r, x0, W.bits_v, lo, pv);
+        ptx::fence_proxy_async_smem();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            uint8_t* to = W.images + ((long long)blockIdx.y * W.tiles + t) * (2 * C::TB);
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(ptx::smem_u32(smem)),
+                         "r"(2 * C::TB)
+                         : "memory");
+            ptx::bulk_commit();
+            ptx::bulk_wait<0>();
+        }
+    }
+    griddep_launch_dependents();
+}
+
 template <int D>
 __global__ void __launch_bounds__(tile::THREADS, 1)
     paged_attn_tile_kernel(const __grid_constant__ PagedAttnParams P, const __grid_constant__ TileWork W) {
@@ -329,8 +373,8 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
     uint32_t* sg = reinterpret_cast<uint32_t*>(smem + C::OFF_SG);
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(bar(K_FULL + s), tile::DQ_WARPS);
-            ptx::mbar_init(bar(V_FULL + s), tile::DQ_WARPS);
+            ptx::mbar_init(bar(K_FULL + s), W.images ? 1 : tile::DQ_WARPS);
+            ptx::mbar_init(bar(V_FULL + s), W.images ? 1 : tile::DQ_WARPS);
             ptx::mbar_init(bar(K_EMPTY + s), 1);
             ptx::mbar_init(bar(V_EMPTY + s), 1);
             ptx::mbar_init(bar(S_FULL + s), 1);
@@ -498,7 +542,7 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                             const float a = __uint_as_float(w[2 * e]), d = __uint_as_float(w[2 * e + 1]);
                             mt[e & 1] = fmaxf(mt[e & 1], fmaxf(a, d));
                             const float2 x = __fadd2_rn(make_float2(a, d), make_float2(-mu, -mu));
-                            const float2 y = make_float2(tile::ex2(x.x), tile::ex2(x.y));
+                            const float2 y = make_float2(ex2(x.x), ex2(x.y));
                             s2[e & 1] = __fadd2_rn(s2[e & 1], y);
                             p[8 * c + e] = pack_half2(y.x, y.y);
                         }
@@ -510,7 +554,7 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                 const bool grow = mt > mx + tile::kLazy || (mx == -INFINITY && mt > -INFINITY);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float mn = fmaxf(mx, mt);
-                    const float f = mx == -INFINITY ? 0.f : tile::ex2(mx - mn);  // (O is 0 or unset while mx is -inf)
+                    const float f = mx == -INFINITY ? 0.f : ex2(mx - mn);  // (O is 0 or unset while mx is -inf)
                     l *= f;
                     mx = mn;
                     if (j > 0) {
@@ -645,6 +689,35 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
             }
             return ((((long long)pg * P.Hkv + h) << P.lg_page) | (tok & ((1 << P.lg_page) - 1)));
         };
+        if (W.images) {
+            // one thread fetches the images; the other warps wait for it at the barrier below
+            if (warp == 8) {
+                griddep_wait();  // (the expanding kernel)
+                const bool one = tile::elect();
+                const uint8_t* img = W.images + ((long long)blockIdx.x * W.tiles + ta) * (2 * C::TB);
+                for (int t = 0; t < n; ++t) {
+                    const int st = t & 1;
+                    if (t >= 2 && !wait(K_EMPTY + st, ((t >> 1) - 1) & 1)) break;
+                    if (one) {
+                        ptx::mbar_arrive_expect_tx(bar(K_FULL + st), C::TB);
+                        ptx::bulk_load(sbase + C::OFF_K + st * C::TB, img + (long long)t * (2 * C::TB), C::TB, bar(K_FULL + st));
+                    }
+                    if (t >= 2 && !wait(V_EMPTY + st, ((t >> 1) - 1) & 1)) break;
+                    if (one) {
+                        ptx::mbar_arrive_expect_tx(bar(V_FULL + st), C::TB);
+                        ptx::bulk_load(sbase + C::OFF_V + st * C::TB, img + (long long)t * (2 * C::TB) + C::TB, C::TB, bar(V_FULL + st));
+                    }
+                    __syncwarp();
+                }
+                // a wait that ran out: the copies it leaves land before the CTA ends
+                if (failed)
+                    for (int st = 0; st < 2; ++st)
+                        for (int ph = 0; ph < 2; ++ph) {
+                            ptx::mbar_spin_bounded(bar(K_FULL + st), ph, 1u << 16);
+                            ptx::mbar_spin_bounded(bar(V_FULL + st), ph, 1u << 16);
+                        }
+            }
+        } else {
         tile::Piece<DP> pk, pv;
         long long row = row_of(0);
         tile::load_piece<D, DP>(P.kc, P.ks, row, x0, W.bits_k, P.sfmt, P.lg_group, pk);
@@ -666,13 +739,17 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
             tile::load_piece<D, DP>(P.vc, P.vs, row, x0, W.bits_v, P.sfmt, P.lg_group, pv);
             row = row_of(t + 2);
         }
+        }
         if (W.n_parts == 1 && !failed) {
             // R_s for the way back, where the K tiles were (d = 256: and the V tiles), once their last MMAs are done:
             // rows n of 64 inputs, the MN-major B operand
-            for (int t = max(0, n - 2); t < n; ++t) {
-                wait(K_EMPTY + (t & 1), (t >> 1) & 1);
-                if (NQ == 1) wait(V_EMPTY + (t & 1), (t >> 1) & 1);
-            }
+            // (with images only the fetching warp has followed the stages' phases)
+            if (!W.images || warp == 8)
+                for (int t = max(0, n - 2); t < n; ++t) {
+                    wait(K_EMPTY + (t & 1), (t >> 1) & 1);
+                    if (NQ == 1) wait(V_EMPTY + (t & 1), (t >> 1) & 1);
+                }
+            if (W.images) ptx::named_bar_sync(1, 256);
             if (!failed) {
                 for (int c = dt; c < D * (D / 8); c += 256) {
                     const int nr = c / (D / 8), ch = c % (D / 8);
@@ -801,8 +878,25 @@ static int launch_tile(const PagedAttnParams& P, const TileWork& W, int blocks, 
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(paged_attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e == cudaSuccess) {
-        paged_attn_tile_kernel<D><<<dim3(P.B * P.Hkv, blocks, W.n_splits), tile::THREADS, C::SMEM, stream>>>(P, W);
-        e = cudaGetLastError();
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        cfg.stream = stream;
+        if (W.images) {
+            cfg.gridDim = dim3(W.tiles, P.B * P.Hkv);
+            cfg.blockDim = dim3(256);
+            cfg.dynamicSmemBytes = 2 * C::TB + 1024;
+            e = cudaFuncSetAttribute(paged_expand_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * C::TB + 1024);
+            if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, paged_expand_kernel<D>, P, W);
+            // the tile kernel turns its q rows while the last tiles are laid down
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+        }
+        cfg.gridDim = dim3(P.B * P.Hkv, blocks, W.n_splits);
+        cfg.blockDim = dim3(tile::THREADS);
+        cfg.dynamicSmemBytes = C::SMEM;
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, paged_attn_tile_kernel<D>, P, W);
     }
     if (e != cudaSuccess) {
         set_error("paged attention launch failed: %s", cudaGetErrorString(e));
