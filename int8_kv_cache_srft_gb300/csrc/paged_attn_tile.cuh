@@ -366,20 +366,26 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     auto bar = [&](int i) { return ptx::smem_u32(&bars[i]); };
-    constexpr int K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, P_FULL = 10, PV_DONE = 12, ROT = 14,
-                  R_FULL = 15, EP_FULL = 16, OUT_FULL = 17, N_BARS = 18;
+    // READY + 2 i + (j & 1): all that stream i's MMAs of step j need: its P, the V tile of the step and the K tile of
+    // the S that follows.  One barrier, and so one wait of the MMA warp: a wait costs the tensor cores 105 idle cycles
+    // even when it finds the phase complete.  Two of them in turn, so that an arrival for step j cannot land in the
+    // phase of step j - 1; what frees the K and V stages of step j also completes step j - 2.
+    // S_DONE, PV_DONE + 2 i + (j & 1): the S and the P.V of step j of stream i, which also free the K and V tile (with
+    // two streams on a tile: stream 1's, the later one).
+    constexpr int K_FIRST = 0, S_DONE = 2, PV_DONE = 6, READY = 10, ROT = 14, R_FULL = 15, EP_FULL = 16, OUT_FULL = 17,
+                  N_BARS = 18;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&bars[N_BARS]);
     float2* tw = reinterpret_cast<float2*>(smem + C::OFF_TW);
     uint32_t* sg = reinterpret_cast<uint32_t*>(smem + C::OFF_SG);
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(bar(K_FULL + s), W.images ? 1 : tile::DQ_WARPS);
-            ptx::mbar_init(bar(V_FULL + s), W.images ? 1 : tile::DQ_WARPS);
-            ptx::mbar_init(bar(K_EMPTY + s), 1);
-            ptx::mbar_init(bar(V_EMPTY + s), 1);
-            ptx::mbar_init(bar(S_FULL + s), 1);
-            ptx::mbar_init(bar(P_FULL + s), 4);
-            ptx::mbar_init(bar(PV_DONE + s), 1);
+            const int tile_arrivals = W.images ? 1 : tile::DQ_WARPS;
+            ptx::mbar_init(bar(K_FIRST + s), tile_arrivals);
+            for (int i = 0; i < 2; ++i) ptx::mbar_init(bar(READY + 2 * i + s), 4 + (i == 0 || dual ? 2 * tile_arrivals : 0));
+            for (int i = 0; i < 2; ++i) {
+                ptx::mbar_init(bar(S_DONE + 2 * i + s), 1);
+                ptx::mbar_init(bar(PV_DONE + 2 * i + s), 1);
+            }
         }
         ptx::mbar_init(bar(ROT), 1);
         ptx::mbar_init(bar(R_FULL), tile::DQ_WARPS);
@@ -483,8 +489,19 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
     __syncthreads();
     tc::fence_after_sync();
 
-    const int n0 = dual ? (n + 1) / 2 : n;  // steps of stream 0
     auto steps_of = [&](int i) { return dual ? (n + 1 - i) / 2 : n; };
+    // the barrier that tile t's K and V arrive on, and whether the step of its V is its stream's last but `ahead`
+    constexpr int AHEAD = NQ == 2 ? 1 : 2;  // steps between a P.V and the S issued after it
+    auto v_bar = [&](int t) { return dual ? READY + 2 * (t & 1) + ((t >> 1) & 1) : READY + (t & 1); };
+    auto k_bar = [&](int t) {
+        if (dual) return t < 2 ? K_FIRST + t : READY + 2 * (t & 1) + (((t >> 1) - 1) & 1);
+        return t < AHEAD ? K_FIRST + t : READY + ((t - AHEAD) & 1);
+    };
+    // tile t's K (V) was read: the barrier, and its phase's parity
+    const int last = NQ == 2 ? 1 : 0;
+    auto freed = [&](int which, int t) { return dual ? which + 2 * (t & 1) + ((t >> 1) & 1) : which + 2 * last + (t & 1); };
+    auto freed_parity = [&](int t) -> uint32_t { return dual ? (t >> 2) & 1 : (t >> 1) & 1; };
+    auto no_next_k = [&](int t) { return t + (dual ? 2 : AHEAD) >= n; };  // the barrier of V t gets its K arrivals bare
     auto wait = [&](int which, uint32_t parity) -> bool {  // a whole warp, converged afterwards
         if (__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(which), parity))) return true;
         failed = true;
@@ -510,7 +527,7 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
         const int steps = steps_of(i);
         for (int j = 0; j < steps; ++j) {
             const int sb = NQ == 2 ? i : (j & 1);
-            if (!wait(S_FULL + sb, NQ == 2 ? (j & 1) : ((j >> 1) & 1))) break;
+            if (!wait(S_DONE + 2 * i + (j & 1), (j >> 1) & 1)) break;
             if (any_live) {
                 tc::fence_after_sync();
                 const int t0 = (ta + (dual ? 2 * j + i : j)) * BN;
@@ -558,7 +575,7 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                     l *= f;
                     mx = mn;
                     if (j > 0) {
-                        if (!wait(PV_DONE + (NQ == 2 ? i : 0), (j - 1) & 1)) break;
+                        if (!wait(PV_DONE + 2 * i + ((j - 1) & 1), ((j - 1) >> 1) & 1)) break;
                         tc::fence_after_sync();
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
@@ -579,14 +596,11 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                 tc::fence_before_sync();
             }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(P_FULL + sb));
+            if (lane == 0) ptx::mbar_arrive(bar(READY + 2 * i + (j & 1)));
         }
         // ---- the end: O / l rotated back, or a partial result ----
         if (!failed && steps > 0) {
-            // one q tile: the last S was issued before the P.V of the step before it, so that phase has to be seen
-            // first (a parity tells two phases apart, not three)
-            if (NQ == 1 && steps > 1) wait(PV_DONE, (steps - 2) & 1);
-            if (!failed && wait(PV_DONE + (NQ == 2 ? i : 0), (steps - 1) & 1)) tc::fence_after_sync();
+            if (wait(PV_DONE + 2 * i + ((steps - 1) & 1), ((steps - 1) >> 1) & 1)) tc::fence_after_sync();
         }
         if (W.n_parts > 1) {
             if (!failed && live) {
@@ -697,25 +711,23 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                 const uint8_t* img = W.images + ((long long)blockIdx.x * W.tiles + ta) * (2 * C::TB);
                 for (int t = 0; t < n; ++t) {
                     const int st = t & 1;
-                    if (t >= 2 && !wait(K_EMPTY + st, ((t >> 1) - 1) & 1)) break;
+                    if (t >= 2 && !wait(freed(S_DONE, t - 2), freed_parity(t - 2))) break;
                     if (one) {
-                        ptx::mbar_arrive_expect_tx(bar(K_FULL + st), C::TB);
-                        ptx::bulk_load(sbase + C::OFF_K + st * C::TB, img + (long long)t * (2 * C::TB), C::TB, bar(K_FULL + st));
+                        ptx::mbar_arrive_expect_tx(bar(k_bar(t)), C::TB);
+                        ptx::bulk_load(sbase + C::OFF_K + st * C::TB, img + (long long)t * (2 * C::TB), C::TB, bar(k_bar(t)));
                     }
-                    if (t >= 2 && !wait(V_EMPTY + st, ((t >> 1) - 1) & 1)) break;
+                    if (t >= 2 && !wait(freed(PV_DONE, t - 2), freed_parity(t - 2))) break;
                     if (one) {
-                        ptx::mbar_arrive_expect_tx(bar(V_FULL + st), C::TB);
-                        ptx::bulk_load(sbase + C::OFF_V + st * C::TB, img + (long long)t * (2 * C::TB) + C::TB, C::TB, bar(V_FULL + st));
+                        ptx::mbar_arrive_expect_tx(bar(v_bar(t)), C::TB);
+                        ptx::bulk_load(sbase + C::OFF_V + st * C::TB, img + (long long)t * (2 * C::TB) + C::TB, C::TB, bar(v_bar(t)));
+                        if (no_next_k(t)) ptx::mbar_arrive(bar(v_bar(t)));
                     }
                     __syncwarp();
                 }
                 // a wait that ran out: the copies it leaves land before the CTA ends
+                // (their barriers may miss other arrivals, so time stands in for them: about 30 ms)
                 if (failed)
-                    for (int st = 0; st < 2; ++st)
-                        for (int ph = 0; ph < 2; ++ph) {
-                            ptx::mbar_spin_bounded(bar(K_FULL + st), ph, 1u << 16);
-                            ptx::mbar_spin_bounded(bar(V_FULL + st), ph, 1u << 16);
-                        }
+                    for (int k = 0; k < 30000; ++k) __nanosleep(1000);
             }
         } else {
         tile::Piece<DP> pk, pv;
@@ -725,17 +737,20 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
         row = row_of(1);
         for (int t = 0; t < n; ++t) {
             const int st = t & 1;
-            if (t >= 2 && !wait(K_EMPTY + st, ((t >> 1) - 1) & 1)) break;
+            if (t >= 2 && !wait(freed(S_DONE, t - 2), freed_parity(t - 2))) break;
             tile::store_piece_any<D, BN, DP>(smem + C::OFF_K + st * C::TB, r, x0, W.bits_k, lo, pk);
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(K_FULL + st));
+            if (lane == 0) ptx::mbar_arrive(bar(k_bar(t)));
             tile::load_piece<D, DP>(P.kc, P.ks, row, x0, W.bits_k, P.sfmt, P.lg_group, pk);
-            if (t >= 2 && !wait(V_EMPTY + st, ((t >> 1) - 1) & 1)) break;
+            if (t >= 2 && !wait(freed(PV_DONE, t - 2), freed_parity(t - 2))) break;
             tile::store_piece_any<D, BN, DP>(smem + C::OFF_V + st * C::TB, r, x0, W.bits_v, lo, pv);
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(V_FULL + st));
+            if (lane == 0) {
+                ptx::mbar_arrive(bar(v_bar(t)));
+                if (no_next_k(t)) ptx::mbar_arrive(bar(v_bar(t)));
+            }
             tile::load_piece<D, DP>(P.vc, P.vs, row, x0, W.bits_v, P.sfmt, P.lg_group, pv);
             row = row_of(t + 2);
         }
@@ -746,8 +761,8 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
             // (with images only the fetching warp has followed the stages' phases)
             if (!W.images || warp == 8)
                 for (int t = max(0, n - 2); t < n; ++t) {
-                    wait(K_EMPTY + (t & 1), (t >> 1) & 1);
-                    if (NQ == 1) wait(V_EMPTY + (t & 1), (t >> 1) & 1);
+                    wait(freed(S_DONE, t), freed_parity(t));
+                    if (NQ == 1) wait(freed(PV_DONE, t), freed_parity(t));
                 }
             if (W.images) ptx::named_bar_sync(1, 256);
             if (!failed) {
@@ -782,63 +797,42 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
             for (int ks = 0; ks < BN / 16; ++ks)
                 tc::mma_f16_ta(dst, pa + 8 * ks, tile::desc(bo + ks * 128), tile::idesc(128, D, true), !(first && ks == 0));
         };
-        if constexpr (NQ == 2) {
-            auto start_s = [&](int i, int j) -> bool {  // S of stream i, step j; false: a wait ran out
+        auto ready = [&](int which, uint32_t parity) -> bool {
+            if (__all_sync(0xffffffffu, ptx::mbar_test_bounded(bar(which), parity))) return true;
+            failed = true;
+            return false;
+        };
+        // S of stream i, step j (its K tile is there)
+        auto start_s = [&](int i, int j) {
+            const int t = dual ? 2 * j + i : j;
+            if (t >= n) return;
+            if (one) {
+                issue_s(NQ == 2 ? i : (j & 1), dual ? 0 : i, t);
+                tc::commit(bar(S_DONE + 2 * i + (j & 1)));
+            }
+            __syncwarp();
+        };
+        bool ok = ready(K_FIRST, 0) && (!(dual || NQ == 1) || n < 2 || ready(K_FIRST + 1, 0));
+        if (ok) {
+            tc::fence_after_sync();
+            start_s(0, 0);
+            if (NQ == 2) start_s(1, 0);
+            else start_s(0, 1);
+        }
+        for (int j = 0; ok && j < steps_of(0); ++j)
+            for (int i = 0; ok && i < NQ; ++i) {
                 const int t = dual ? 2 * j + i : j;
-                if (t >= n) return true;
-                if ((i == 0 || dual) && !wait(K_FULL + (t & 1), (t >> 1) & 1)) return false;
-                tc::fence_after_sync();
-                if (one) {
-                    issue_s(i, dual ? 0 : i, t);
-                    if (i == 1 || dual) tc::commit(bar(K_EMPTY + (t & 1)));
-                    tc::commit(bar(S_FULL + i));
-                }
-                __syncwarp();
-                return true;
-            };
-            bool ok = start_s(0, 0) && start_s(1, 0);
-            for (int j = 0; ok && j < n0; ++j)
-                for (int i = 0; ok && i < 2; ++i) {
-                    const int t = dual ? 2 * j + i : j;
-                    if (t >= n) continue;
-                    ok = ((i == 1 && !dual) || wait(V_FULL + (t & 1), (t >> 1) & 1)) && wait(P_FULL + i, j & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    if (one) {
-                        issue_pv(i, i * D, t, j == 0);
-                        tc::commit(bar(PV_DONE + i));
-                        if (i == 1 || dual) tc::commit(bar(V_EMPTY + (t & 1)));
-                    }
-                    __syncwarp();
-                    ok = start_s(i, j + 1);
-                }
-        } else {
-            auto start_s = [&](int t) -> bool {
-                if (t >= n) return true;
-                if (!wait(K_FULL + (t & 1), (t >> 1) & 1)) return false;
-                tc::fence_after_sync();
-                if (one) {
-                    issue_s(t & 1, 0, t);
-                    tc::commit(bar(K_EMPTY + (t & 1)));
-                    tc::commit(bar(S_FULL + (t & 1)));
-                }
-                __syncwarp();
-                return true;
-            };
-            bool ok = start_s(0) && start_s(1);
-            for (int t = 0; ok && t < n; ++t) {
-                ok = wait(V_FULL + (t & 1), (t >> 1) & 1) && wait(P_FULL + (t & 1), (t >> 1) & 1);
+                if (t >= n) continue;
+                ok = ready(READY + 2 * i + (j & 1), (j >> 1) & 1);
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (one) {
-                    issue_pv(t & 1, 0, t, t == 0);
-                    tc::commit(bar(PV_DONE));
-                    tc::commit(bar(V_EMPTY + (t & 1)));
+                    issue_pv(NQ == 2 ? i : (j & 1), NQ == 2 ? i * D : 0, t, j == 0);
+                    tc::commit(bar(PV_DONE + 2 * i + (j & 1)));
                 }
                 __syncwarp();
-                ok = start_s(t + 2);
+                start_s(i, j + AHEAD);
             }
-        }
         if (W.n_parts == 1 && !failed && wait(R_FULL, 0) && wait(EP_FULL, 0)) {
             tc::fence_after_sync();
             if (one) {
