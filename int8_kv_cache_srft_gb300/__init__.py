@@ -317,7 +317,7 @@ class PagedBatch:
 
 def _rows_arg(fn: str, name: str, x: torch.Tensor, n: int, H: int, d: int, dtype, device) -> int:
     """The token stride of rows [n][H][d]; raises when they are not rows the library can take."""
-    if tuple(x.shape) != (n, H, d) or x.dtype != dtype:
+    if x.shape != (n, H, d) or x.dtype != dtype:
         _invalid(fn, f"{name} must be [{n}][{H}][{d}] of one 16-bit type, got {tuple(x.shape)} {x.dtype}")
     s0, s1, s2 = x.stride()
     if n * H and (s2 != 1 or (s1 != d and H > 1)):
@@ -327,18 +327,22 @@ def _rows_arg(fn: str, name: str, x: torch.Tensor, n: int, H: int, d: int, dtype
     return s0 if n > 1 else 0
 
 
-def _paged_device(fn: str, pages: Pages):
+def _paged_device(fn: str, pages: Pages, stream):
+    """The pools' device, which has to be the current one, and the stream of the call."""
     dev = pages.codes.device
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        _invalid(fn, f"the pools are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return dev
+    if dev.type != "cuda":
+        return dev, None
+    now = torch.cuda.current_device()
+    if dev.index != now:
+        _invalid(fn, f"the pools are on {dev}, the current device is cuda:{now}")
+    return dev, _raw_stream(now) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _paged_codec(fn: str, k: Pages | None, xk, v: Pages | None, xv, slots: torch.Tensor, sign_seed: int, stream):
     side = k if k is not None else v
     if side is None:
         _invalid(fn, "at least one of k, v must be given")
-    dev = _paged_device(fn, side)
+    dev, stream = _paged_device(fn, side, stream)
     if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous() or slots.device != dev:
         _invalid(fn, "slots must be a contiguous int64 [n_tokens] on the pools' device")
     n, H, dtype = slots.shape[0], side.codes.shape[1], (xk if k is not None else xv).dtype
@@ -349,7 +353,7 @@ def _paged_codec(fn: str, k: Pages | None, xk, v: Pages | None, xv, slots: torch
     lib = library()
     rc = getattr(lib, fn)(k.c_pointer() if k is not None else None, xk.data_ptr() if k is not None else None, sk,
                           v.c_pointer() if v is not None else None, xv.data_ptr() if v is not None else None, sv,
-                          slots.data_ptr(), n, DTYPES[dtype], sign_seed, _stream(stream))
+                          slots.data_ptr(), n, DTYPES[dtype], sign_seed, stream)
     if rc:
         _check(fn, rc)
 
@@ -375,7 +379,7 @@ def q4kv_paged_attention(q: torch.Tensor, out: torch.Tensor, k: Pages, v: Pages,
                          window: int, sign_seed: int, workspace: torch.Tensor, stream=None) -> None:
     """Causal attention of the query rows q [total_q][Hq][d] over the pages; out like q (see include/srftkv.h)."""
     fn = "q4kv_paged_attention"
-    dev = _paged_device(fn, k)
+    dev, stream = _paged_device(fn, k, stream)
     if q.dtype not in DTYPES or q.dim() != 3:
         _invalid(fn, f"q must be [total_q][Hq][d] of fp16 or bf16, got {tuple(q.shape)} {q.dtype}")
     b = batch.c_pointer()
@@ -386,7 +390,7 @@ def q4kv_paged_attention(q: torch.Tensor, out: torch.Tensor, k: Pages, v: Pages,
         _invalid(fn, "the pools, the batch's tables and the workspace must be on one device")
     rc = library().q4kv_paged_attention(q.data_ptr(), qs, out.data_ptr(), os, DTYPES[q.dtype], Hq, k.c_pointer(),
                                         v.c_pointer(), b, sm_scale, window, sign_seed, workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(), _stream(stream))
+                                        workspace.nbytes, stream)
     if rc:
         _check(fn, rc)
 

@@ -117,6 +117,17 @@ int device_sm_count() {
     return n > 0 ? n : 1;
 }
 
+cudaError_t allow_smem(std::atomic<unsigned long long>& done, const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
+}
+
 // ---------------------------------------------------------------------------
 // Device addresses of the library's __device__ variables, per CUDA context
 // ---------------------------------------------------------------------------

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
@@ -73,6 +74,8 @@ struct SymbolCache {
 };
 int symbol_address(SymbolCache& cache, const void* symbol, void** out, const char* what);
 int device_sm_count();
+// Raise a kernel's dynamic shared memory limit, once per kernel and device (`done`: one bit a device).
+cudaError_t allow_smem(std::atomic<unsigned long long>& done, const void* kernel, int bytes);
 int current_device_ok();  // SRFTKV_OK, or the error code with the message set
 
 // Generic tiled tensor map (element strides 1); false + message on failure.

@@ -18,38 +18,48 @@ static __device__ unsigned int g_paged_attn_fault;
 
 // Join the partial results of one (query token, head), one warp a row:
 // o = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p, then / lambda_V and R^T.
-// Partials with m = -inf are empty and their acc is not read.
+// Partials with m = -inf are empty and their acc counts for nothing.
 template <int D, typename T>
 __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_constant__ PagedAttnParams P, int n_parts,
                                                                  const float* __restrict__ part_ml,
                                                                  const float* __restrict__ part_acc) {
     constexpr int E = D / 32;
     __shared__ float2 sm[4][D / 2];
-    griddep_wait();  // the partial results first
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y;
     const long long u = (long long)blockIdx.x * 4 + warp;
     const int i = (int)(u / P.Hq), hq = (int)(u - (long long)i * P.Hq), h = hq / P.rep;
     const int q0 = P.cu_q ? P.cu_q[b] : b;
     const int m = min(P.cu_q ? P.cu_q[b + 1] - q0 : 1, P.max_q);
+    griddep_wait();  // the partial results
     if (i >= m || q0 < 0 || q0 + i >= P.total_q) return;
     const long long at = ((long long)(q0 + i) * P.Hq + hq) * n_parts;
-    float M = -INFINITY;
-    for (int p = lane; p < n_parts; p += 32) M = fmaxf(M, part_ml[2 * (at + p)]);
+    // four partials at a time, their loads all at once; an empty one's acc holds anything and is not used
+    float M = -INFINITY, o[E] = {}, l = 0.f;
+    for (int p0 = 0; p0 < n_parts; p0 += 4) {
+        float2 ml[4];
+        float a[4][E];
 #pragma unroll
-    for (int k = 16; k; k >>= 1) M = fmaxf(M, rot::sx(M, k));
-    float o[E] = {}, l = 0.f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-        for (int p = 0; p < n_parts; ++p) {
-            const float2 ml = *reinterpret_cast<const float2*>(part_ml + 2 * (at + p));
-            if (ml.x == -INFINITY) continue;
-            const float w = exp2f(ml.x - M);
-            l = fmaf(w, ml.y, l);
-            float a[E];
-            rot::load_lambda<D>(part_acc + (at + p) * D, lane, a);
+        for (int k = 0; k < 4; ++k) {
+            const int p = min(p0 + k, n_parts - 1);
+            ml[k] = __ldg(reinterpret_cast<const float2*>(part_ml) + at + p);
+            rot::load_lambda<D>(part_acc + (at + p) * D, lane, a[k]);
+            if (p0 + k >= n_parts) ml[k].x = -INFINITY;
+        }
+        const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+        if (mn == -INFINITY) continue;
+        const float f = exp2f(M - mn);
+        M = mn;
+        l *= f;
 #pragma unroll
-            for (int j = 0; j < E; ++j) o[j] = fmaf(w, a[j], o[j]);
+        for (int j = 0; j < E; ++j) o[j] *= f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (ml[k].x == -INFINITY) continue;
+            const float w = exp2f(ml[k].x - mn);
+            l = fmaf(w, ml[k].y, l);
+#pragma unroll
+            for (int j = 0; j < E; ++j) o[j] = fmaf(w, a[k][j], o[j]);
         }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -80,11 +90,14 @@ struct Plan {
 // The most workspace that laying tiles down may take (an eighth of it is what one layer of 128 k tokens and 2 kv heads
 // takes); past it they are turned where they are used.
 constexpr size_t kMaxImages = 1ull << 30;
-static Plan make_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window) {
+static Plan work_out_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window, int sm_count) {
     Plan p = {};
     const int rep = Hq / Hkv;
-    const long long rows = (long long)max_q * rep, sms = device_sm_count();
-    p.few = rows <= 8;
+    const long long rows = (long long)max_q * rep, sms = sm_count;
+    // 8 ragged sequences of 9 k to 32 k tokens, 8 kv heads, int4: the split kernel reads the cache once for every 8 rows
+    // (d = 256: 4), the tile kernel once for 128; d = 64: 197 us against 225 at 40 rows, 233 against 226 at 48; d = 128:
+    // 223 against 277 at 20 rows, 288 against 270 at 32; d = 256: 501 against 617 at 24, 663 against 619 at 32
+    p.few = rows <= (d == 64 ? 40 : 28);
     if (p.few) {
         p.S.nr = rows > 4 && d <= 128 ? 2 : 1;
         p.S.groups = (int)((rows + 4 * p.S.nr - 1) / (4 * p.S.nr));
@@ -92,15 +105,14 @@ static Plan make_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q, int
         long long see = max_len;
         if (window) see = std::min<long long>(see, (long long)window + max_q - 1 + 31);
         const long long base = (long long)B * Hkv * p.S.groups;
-        // two or three CTAs run on an SM: the split count that shortens waves * (tokens a split + its fixed part, the
-        // rotation, fragments and join, worth about 256 tokens of one CTA)
-        const long long at_once = (d == 256 || p.S.nr == 2 ? 2 : 3) * sms, fixed = 256;
-        long long tokens = 0, best_cost = -1;
-        for (long long s = 1; s <= std::min<long long>((see + 127) / 128, 256); ++s) {
-            const long long t = ((see + s - 1) / s + 127) / 128 * 128, n = (see + t - 1) / t;
-            const long long cost = (base * n + at_once - 1) / at_once * (t + fixed);
-            if (best_cost < 0 || cost < best_cost) tokens = t, best_cost = cost;
-        }
+        // Two or three CTAs run on an SM.  Lengths are ragged in earnest and max_seq_len is only their bound, so a split
+        // is a quarter of what one CTA would get if they were all the longest (the scheduler evens the rest out), but
+        // no less than 512 tokens (the rotation, fragments and join are worth about 256), unless one wave holds
+        // all of them anyway (24 sequences of 1 to 9215 tokens: 66 us with a quarter, 68 with a half, 81 with all of it).
+        const long long at_once = (d == 256 ? 2 : 3) * sms;
+        const long long even = (see * base + at_once - 1) / at_once;  // tokens of a CTA in one wave
+        long long tokens = std::max(even / 4, std::min<long long>(even, 512));
+        tokens = (std::min(tokens, see) + 127) / 128 * 128;
         p.S.tokens = (int)tokens;
         p.S.n_splits = (int)((see + tokens - 1) / tokens);
         p.n_parts = p.S.n_parts = p.S.n_splits;
@@ -143,6 +155,21 @@ static Plan make_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q, int
         }
     }
     return p;
+}
+
+// (the last one of this host thread is kept: a decode loop asks for the same one every call, twice)
+static const Plan& make_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window) {
+    struct Key {
+        int v[9];
+    };
+    thread_local Key last = {};
+    thread_local Plan plan = {};
+    const Key k = {{d, Hq, Hkv, B, total_q, max_q, max_len, window, device_sm_count()}};
+    if (!std::equal(k.v, k.v + 9, last.v)) {
+        plan = work_out_plan(d, Hq, Hkv, B, total_q, max_q, max_len, window, k.v[8]);
+        last = k;
+    }
+    return plan;
 }
 
 size_t paged_attention_workspace(int d, int Hq, int Hkv, int B, int total_q, int max_q, int max_len, int window) {

@@ -859,6 +859,7 @@ static int launch_tile(const PagedAttnParams& P, const TileWork& W, int blocks, 
     using C = tile::Cfg<D>;
     // the registers the warps pass to each other are counted on kRegs at launch: another count would leave some waiting
     static std::atomic<int> regs{0};
+    static std::atomic<unsigned long long> done{0}, done_expand{0};
     cudaError_t e = cudaSuccess;
     if (regs.load() == 0) {
         cudaFuncAttributes at;
@@ -870,7 +871,7 @@ static int launch_tile(const PagedAttnParams& P, const TileWork& W, int blocks, 
         return SRFTKV_ERR_CUDA;
     }
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(paged_attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        e = allow_smem(done, reinterpret_cast<const void*>(paged_attn_tile_kernel<D>), C::SMEM);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
@@ -879,7 +880,7 @@ static int launch_tile(const PagedAttnParams& P, const TileWork& W, int blocks, 
             cfg.gridDim = dim3(W.tiles, P.B * P.Hkv);
             cfg.blockDim = dim3(256);
             cfg.dynamicSmemBytes = 2 * C::TB + 1024;
-            e = cudaFuncSetAttribute(paged_expand_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * C::TB + 1024);
+            e = allow_smem(done_expand, reinterpret_cast<const void*>(paged_expand_kernel<D>), 2 * C::TB + 1024);
             if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, paged_expand_kernel<D>, P, W);
             // the tile kernel turns its q rows while the last tiles are laid down
             attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

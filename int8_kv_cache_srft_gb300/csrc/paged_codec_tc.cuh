@@ -8,9 +8,10 @@
 //           scales, rounding and packing, one thread a row and 32 columns
 //   read:   X = P . R_s, P = code * scale / lambda rounded to fp16 once
 //
-// Warps: 0-7 bring a tile in (write: 16-bit rows, coalesced; read: codes and
-// scales turned into P) and lay it down as the swizzled A operand; 16 issues
-// the MMAs into a ring of accumulators; 8-15 take them out.
+// Warps (8 and 16, or 16 and 8): some bring a tile in (write: 16-bit rows,
+// coalesced; read: codes and scales turned into P) and lay it down as the swizzled
+// A operand; the last issues the MMAs into a ring of accumulators; the others take
+// them out.
 //
 // bf16 rows go over to fp16 as they are where their largest value lies in
 // [2^-6, 2^15), else multiplied by the power of two that brings it to [1, 2); the
@@ -26,9 +27,11 @@ namespace srftkv {
 
 namespace ctc {
 
-constexpr int THREADS = 17 * 32;
 template <int D, bool WRITE>
 struct Cfg {
+    // Warps that bring tiles in, and that take them out: the heavier end of each direction gets sixteen (with eight at
+    // both ends a tile took 2 us of dependent instructions, whatever the memory did)
+    static constexpr int NL = WRITE || D < 256 ? 8 : 16, NE = WRITE || D < 256 ? 16 : 8, THREADS = (NL + NE + 1) * 32, MMA = NL + NE;
     static constexpr int NB = WRITE && D == 256 ? 128 : D;  // output columns a CTA (d = 256: half of them)
     static constexpr int NSPLIT = D / NB;
     static constexpr int B_BYTES = NB * D * 2 * (WRITE ? 2 : 1);
@@ -39,15 +42,16 @@ struct Cfg {
     static constexpr bool AHEAD = D <= 128;
     static constexpr int ST = !AHEAD ? 1 : WRITE ? 4 : 3, PD = 2;
     static constexpr int NACC = WRITE || D < 256 ? 4 : 2;       // accumulators of NB columns
-    static constexpr int RAW16 = D / 32 + 1;                    // 16-byte pieces a thread (8-bit codes; scales last)
-    static constexpr int RAW = AHEAD && !WRITE ? RAW16 * 256 * 16 : 0;
+    static constexpr int TPR = NL / 4;                          // read: threads a row
+    static constexpr int RAW16 = D / (16 * TPR) + 1;            // 16-byte pieces a thread (8-bit codes; scales last)
+    static constexpr int RAW = AHEAD && !WRITE ? RAW16 * NL * 512 : 0;
     static constexpr int OFF_A = B_BYTES;
     static constexpr int OFF_RAW = OFF_A + ST * A_BYTES;
     static constexpr int OFF_TW = OFF_RAW + PD * RAW;
     static constexpr int OFF_SG = OFF_TW + D * 8;
     static constexpr int OFF_RF = OFF_SG + D * 2;      // write: 2^e of the rows of eight tiles
     static constexpr int OFF_OUT = OFF_RF + (WRITE ? 8 * 128 * 4 : 0);  // read: 32 rows of 64 bytes for each epilogue warp
-    static constexpr int OFF_BAR = OFF_OUT + (WRITE ? 0 : 8 * 2048);
+    static constexpr int OFF_BAR = OFF_OUT + (WRITE ? 0 : NE * 2048);
     static constexpr int USED = OFF_BAR + 256;
     static constexpr int SMEM = (USED > 120 * 1024 ? USED : 120 * 1024) + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -56,7 +60,8 @@ struct Cfg {
 // n (at most B) bytes from global memory to shared memory and zeros behind them
 template <int B>
 __device__ __forceinline__ void copy(uint32_t dst, const void* src, int n) {
-    if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    if constexpr (B == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -104,16 +109,16 @@ struct CtcCommon {
         uint32_t* sg = reinterpret_cast<uint32_t*>(smem + C::OFF_SG);
         if (threadIdx.x == 0) {
             for (int i = 0; i < C::ST; ++i) {
-                ptx::mbar_init(ptx::smem_u32(&bars[A_FULL + i]), 8);
+                ptx::mbar_init(ptx::smem_u32(&bars[A_FULL + i]), C::NL);
                 ptx::mbar_init(ptx::smem_u32(&bars[A_EMPTY + i]), 1);
             }
             for (int i = 0; i < C::NACC; ++i) {
                 ptx::mbar_init(ptx::smem_u32(&bars[ACC_FULL + i]), 1);
-                ptx::mbar_init(ptx::smem_u32(&bars[ACC_EMPTY + i]), 8);
+                ptx::mbar_init(ptx::smem_u32(&bars[ACC_EMPTY + i]), WRITE ? 4 * (C::NB / 32) : 8);
             }
             ptx::fence_barrier_init();
         }
-        if (warp == 16) {
+        if (warp == C::MMA) {
             tc::tmem_alloc(ptx::smem_u32(slot), 512);
             tc::tmem_relinquish();
         }
@@ -139,7 +144,7 @@ struct CtcCommon {
 
 // DT: SRFTKV_DTYPE_*
 template <int D, int DT>
-__global__ void __launch_bounds__(ctc::THREADS, 1) paged_quantize_tc_kernel(const __grid_constant__ PagedCodecParams P) {
+__global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_tc_kernel(const __grid_constant__ PagedCodecParams P) {
     using S = CtcCommon<D, true>;
     using C = typename S::C;
     extern __shared__ uint8_t smem_raw[];
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_quantize_tc_kernel(cons
     const uint32_t tmem = *slot;
     bool failed = false;
 
-    if (warp < 8) {
+    if (warp < C::NL) {
         // 16 rows a warp; a step covers 32 / (D / 8) rows, 16 bytes a lane; each lane lays down, and in the bf16 case
         // later converts in place, its own pieces
         constexpr int LPR = D / 8, RPS = LPR >= 32 ? 1 : 32 / LPR, NI = 16 * LPR / 32, PD = C::PD;
@@ -245,11 +250,13 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_quantize_tc_kernel(cons
             }
         }
         if constexpr (C::AHEAD) ctc::wait_copies<0>();  // (after a wait that ran out some are under way)
-    } else if (warp < 16) {
-        const int quarter = warp & 3, ch = (warp - 8) >> 2;  // lanes 32 quarter ..; column half
-        constexpr int UNITS = C::NB / 64;                    // 32-column units a warp
-        int i_tile = 0;
-        for (int u = first; u < total; u += step, ++i_tile) {
+    } else if (warp < C::MMA) {
+        // a warp: lanes 32 quarter .., 32 columns; where a tile has fewer than four such columns, the warps left over take
+        // every other tile
+        constexpr int UNITS = C::NB / 32, GROUPS = C::NE / 4 / UNITS;
+        const int quarter = warp & 3, unit = ((warp - C::NL) >> 2) % UNITS, group = ((warp - C::NL) >> 2) / UNITS;
+        int i_tile = group;
+        for (int u = first + group * step; u < total; u += GROUPS * step, i_tile += GROUPS) {
             const int a = i_tile % C::NACC;
             const ctc::Tile t = ctc::tile_at(P, u, per_side);
             const PagedSideK& sd = P.side[t.side];
@@ -261,17 +268,14 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_quantize_tc_kernel(cons
             }
             tc::fence_after_sync();
             const float up = DT == SRFTKV_DTYPE_BF16 ? rf[(i_tile & 7) * 128 + r] : 1.f;
-#pragma unroll 1
-            for (int k = 0; k < UNITS; ++k) {
-                const int c0 = 32 * (ch * UNITS + k);
+            {
+                const int c0 = 32 * unit;
                 uint32_t raw[32];
                 tc::ld_32x32b_x32(tmem + ((uint32_t)(32 * quarter) << 16) + a * C::NB + c0, raw);
                 tc::wait_ld(raw);
-                if (k == UNITS - 1) {
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bar(S::ACC_EMPTY + a));
-                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(S::ACC_EMPTY + a));
                 if (row >= 0) {
                     const int col = half * C::NB + c0;
                     float z[32];
@@ -328,11 +332,11 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_quantize_tc_kernel(cons
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 16) tc::tmem_dealloc(tmem, 512);
+    if (warp == C::MMA) tc::tmem_dealloc(tmem, 512);
 }
 
 template <int D, int DT>
-__global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(const __grid_constant__ PagedCodecParams P) {
+__global__ void __launch_bounds__(ctc::Cfg<D, false>::THREADS, 1) paged_dequantize_tc_kernel(const __grid_constant__ PagedCodecParams P) {
     using S = CtcCommon<D, false>;
     using C = typename S::C;
     extern __shared__ uint8_t smem_raw[];
@@ -348,19 +352,18 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(co
     const uint32_t tmem = *slot;
     bool failed = false;
 
-    if (warp < 8) {
-        // two threads a row, D/2 coordinates each in pieces of DP
-        constexpr int DP = D == 64 ? 32 : 64, NP = D / 2 / DP;
-        const int r = threadIdx.x >> 1, x0 = (threadIdx.x & 1) * (D / 2);
-        constexpr int PD = C::PD, U = D / 32;  // U: 16-coordinate units of half a row
-        tile::Piece<DP> p[NP];
+    if (warp < C::NL) {
+        // TPR threads a row, DP coordinates each
+        constexpr int DP = D / C::TPR, PD = C::PD, U = DP / 16;
+        const int r = threadIdx.x / C::TPR, x0 = (threadIdx.x % C::TPR) * DP;
+        tile::Piece<DP> p;
         auto row_of = [&](int u) -> long long {
             if (u >= total) return -1;
             const ctc::Tile t = ctc::tile_at(P, u, per_side);
             return ctc::row_of(P, t.t0 + r, t.h);
         };
         const int ng = D >> P.lg_group;
-        auto raw = [&](int q, int i) { return (uint32_t)(C::OFF_RAW + q * C::RAW + (i * 256 + (int)threadIdx.x) * 16); };
+        auto raw = [&](int q, int i) { return (uint32_t)(C::OFF_RAW + q * C::RAW + (i * C::NL * 32 + (int)threadIdx.x) * 16); };
         auto load = [&](int u, int q, long long row) {  // into the raw ring (or registers)
             if (u < total) {
                 const PagedSideK& sd = P.side[u >= per_side];
@@ -377,9 +380,7 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(co
                         ctc::copy<4>(sbase + raw(q, C::RAW16 - 1) + 4 * i,
                                      sd.scales + (((at * ng + ((x0 + 16 * i) >> P.lg_group)) * sb) & ~3ll), n / 4);
                 } else {
-#pragma unroll
-                    for (int k = 0; k < NP; ++k)
-                        tile::load_piece<D, DP>(sd.codes, sd.scales, row, x0 + k * DP, sd.bits, sd.sfmt, P.lg_group, p[k]);
+                    tile::load_piece<D, DP>(sd.codes, sd.scales, row, x0, sd.bits, sd.sfmt, P.lg_group, p);
                 }
             }
             if constexpr (C::AHEAD) ctc::commit_copies();
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(co
                 for (int i = 0; i < C::RAW16 - 1; ++i)
                     if (i < (C::RAW16 - 1) * sd.bits / 8) {
                         const uint4 t = *reinterpret_cast<const uint4*>(smem + raw(q, i));
-                        p[0].w[4 * i] = t.x, p[0].w[4 * i + 1] = t.y, p[0].w[4 * i + 2] = t.z, p[0].w[4 * i + 3] = t.w;
+                        p.w[4 * i] = t.x, p.w[4 * i + 1] = t.y, p.w[4 * i + 2] = t.z, p.w[4 * i + 3] = t.w;
                     }
                 // where the scale lies in its word: rows of 1 or 2 scales shift with the row (its slot's low bits)
                 int low = 0;
@@ -403,10 +404,10 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(co
                 for (int i = 0; i < U; ++i) {
                     const uint32_t w = *reinterpret_cast<const uint32_t*>(smem + raw(q, C::RAW16 - 1) + 4 * i);
                     const int at = low + ((x0 + 16 * i) >> P.lg_group);
-                    if (sd.sfmt == SRFTKV_SCALE_FP32) p[0].sc[i] = __uint_as_float(w);
+                    if (sd.sfmt == SRFTKV_SCALE_FP32) p.sc[i] = __uint_as_float(w);
                     else if (sd.sfmt == SRFTKV_SCALE_FP16)
-                        p[0].sc[i] = __half2float(__ushort_as_half((unsigned short)(w >> (16 * (at & 1)))));
-                    else p[0].sc[i] = __uint_as_float(((w >> (8 * (at & 3))) & 0xFFu) << 23);
+                        p.sc[i] = __half2float(__ushort_as_half((unsigned short)(w >> (16 * (at & 1)))));
+                    else p.sc[i] = __uint_as_float(((w >> (8 * (at & 3))) & 0xFFu) << 23);
                 }
             }
         };
@@ -430,28 +431,24 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(co
             uint8_t* a = smem + C::OFF_A + s * C::A_BYTES;
             const PagedSideK& sd = P.side[u >= per_side];
             if (sd.lambda == nullptr) {
-#pragma unroll
-                for (int k = 0; k < NP; ++k)
-                    tile::store_piece_any<D, 128, DP>(a, r, x0 + k * DP, sd.bits, sd.sfmt == SRFTKV_SCALE_FP32, p[k]);
+                tile::store_piece_any<D, 128, DP>(a, r, x0, sd.bits, sd.sfmt == SRFTKV_SCALE_FP32, p);
             } else {
                 const float* lam = sd.lambda + (long long)ctc::tile_at(P, u, per_side).h * D + x0;
 #pragma unroll
-                for (int k = 0; k < NP; ++k)
+                for (int g = 0; g < DP / 8; ++g) {  // eight coordinates, in the order of dq_kperm
+                    float f[8];
 #pragma unroll
-                    for (int g = 0; g < DP / 8; ++g) {  // eight coordinates, in the order of dq_kperm
-                        float f[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t w = sd.bits == 4 ? p[k].w[g] : p[k].w[(2 * g + (j >> 2)) % (DP / 4)];
-                            const int sh = sd.bits == 4 ? 28 - 4 * j : 24 - 8 * (j & 3);
-                            const int c = (int)(w << sh) >> (sd.bits == 4 ? 28 : 24);
-                            f[j] = __fdiv_rn((float)c * p[k].sc[g >> 1], __ldg(lam + k * DP + 8 * g + j));
-                        }
-                        const int x = x0 + k * DP + 8 * g;
-                        *reinterpret_cast<uint4*>(a + (x >> 6) * 16384 + r * 128 + ((((x & 63) >> 3) ^ (r & 7)) << 4)) =
-                            make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]),
-                                       pack_half2(f[3], f[7]));
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t w = sd.bits == 4 ? p.w[g] : p.w[(2 * g + (j >> 2)) % (DP / 4)];
+                        const int sh = sd.bits == 4 ? 28 - 4 * j : 24 - 8 * (j & 3);
+                        const int c = (int)(w << sh) >> (sd.bits == 4 ? 28 : 24);
+                        f[j] = __fdiv_rn((float)c * p.sc[g >> 1], __ldg(lam + 8 * g + j));
                     }
+                    const int x = x0 + 8 * g;
+                    *reinterpret_cast<uint4*>(a + (x >> 6) * 16384 + r * 128 + ((((x & 63) >> 3) ^ (r & 7)) << 4)) =
+                        make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]),
+                                   pack_half2(f[3], f[7]));
+                }
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -462,17 +459,24 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(co
             }
         }
         if constexpr (C::AHEAD) ctc::wait_copies<0>();
-    } else if (warp < 16) {
-        const int quarter = warp & 3, c0 = ((warp - 8) >> 2) * (D / 2);
-        uint8_t* stage = smem + C::OFF_OUT + (warp - 8) * 2048;
-        int i_tile = 0;
-        for (int u = first; u < total; u += step, ++i_tile) {
+    } else if (warp < C::MMA) {
+        // a warp: lanes 32 quarter .., half the columns, of every GROUPSth tile
+        constexpr int GROUPS = C::NE / 8;
+        const int quarter = warp & 3, c0 = (((warp - C::NL) >> 2) & 1) * (D / 2), group = (warp - C::NL) >> 3;
+        uint8_t* stage = smem + C::OFF_OUT + (warp - C::NL) * 2048;
+        auto live_at = [&](int u) -> bool {
+            if (u >= total) return false;
+            const ctc::Tile t = ctc::tile_at(P, u, per_side);
+            return ctc::row_of(P, t.t0 + 32 * quarter + lane, t.h) >= 0;
+        };
+        int i_tile = group;
+        bool next = live_at(first + group * step);  // (its slot is looked up a tile ahead)
+        for (int u = first + group * step; u < total; u += GROUPS * step, i_tile += GROUPS) {
             const int a = i_tile % C::NACC;
             const ctc::Tile t = ctc::tile_at(P, u, per_side);
             const PagedSideK& sd = P.side[t.side];
-            const int tok = t.t0 + 32 * quarter + lane;
-            const bool live = ctc::row_of(P, tok, t.h) >= 0;
-            const uint32_t rows = __ballot_sync(0xffffffffu, live);
+            const uint32_t rows = __ballot_sync(0xffffffffu, next);
+            next = live_at(u + GROUPS * step);
             // this lane's place in the coalesced stores: 16-byte piece lane % 4 of rows lane / 4 + 8 j
             uint16_t* x = static_cast<uint16_t*>(sd.x) + (long long)(t.t0 + 32 * quarter + (lane >> 2)) * sd.x_stride +
                           (long long)t.h * D + c0 + 8 * (lane & 3);
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(ctc::THREADS, 1) paged_dequantize_tc_kernel(co
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 16) tc::tmem_dealloc(tmem, 512);
+    if (warp == C::MMA) tc::tmem_dealloc(tmem, 512);
 }
 
 template <int D>
@@ -557,9 +561,10 @@ static int launch_codec_tc(const PagedCodecParams& P, int dtype, bool write, cud
     const int smem = write ? CW::SMEM : CR::SMEM, split = write ? CW::NSPLIT : 1;
     const int total = (P.n_tokens + 127) / 128 * P.H * P.n_sides, sms = device_sm_count();
     const int ctas = total < sms / split ? total : sms / split;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<unsigned long long> done[4];
+    cudaError_t e = allow_smem(done[2 * write + (dtype == SRFTKV_DTYPE_BF16)], reinterpret_cast<const void*>(k), smem);
     if (e == cudaSuccess) {
-        k<<<ctas * split, ctc::THREADS, smem, stream>>>(P);
+        k<<<ctas * split, write ? CW::THREADS : CR::THREADS, smem, stream>>>(P);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) {

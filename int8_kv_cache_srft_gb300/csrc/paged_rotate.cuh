@@ -34,6 +34,10 @@ struct Dim {
 
 // e^{-2 pi i m / 256}, per-lane indices through the L1-served table
 __device__ __forceinline__ float2 twid(int m) { return make_float2(tw_re_lane(m), tw_im_lane(m)); }
+// Bring the twiddle table (2 KB) to L1 while something else is waited for: a warp that turns one row meets it cold
+__device__ __forceinline__ void prefetch_twiddles(int lane) {
+    if (lane < 16) asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const char*>(&g_tw) + 128 * lane));
+}
 __device__ __forceinline__ float sx(float v, int m) { return __shfl_xor_sync(0xffffffffu, v, m); }
 
 // Unnormalised DFT of the warp's N complex points (v[2j], v[2j+1] = point C l + j); INV: conjugate
