@@ -105,13 +105,14 @@ static Plan work_out_plan(int d, int Hq, int Hkv, int B, int total_q, int max_q,
         long long see = max_len;
         if (window) see = std::min<long long>(see, (long long)window + max_q - 1 + 31);
         const long long base = (long long)B * Hkv * p.S.groups;
-        // Two or three CTAs run on an SM.  Lengths are ragged in earnest and max_seq_len is only their bound, so a split
-        // is a quarter of what one CTA would get if they were all the longest (the scheduler evens the rest out), but
+        // Two or three CTAs run on an SM.  Lengths are ragged in earnest and max_seq_len is only their bound, so from
+        // four sequences on a split is a quarter of what one CTA would get if all were the longest (the scheduler evens the
+        // rest out; with one sequence there is nothing to even out: 49 us in one wave, 74 in four, at 20 rows), but
         // no less than 512 tokens (the rotation, fragments and join are worth about 256), unless one wave holds
         // all of them anyway (24 sequences of 1 to 9215 tokens: 66 us with a quarter, 68 with a half, 81 with all of it).
         const long long at_once = (d == 256 ? 2 : 3) * sms;
         const long long even = (see * base + at_once - 1) / at_once;  // tokens of a CTA in one wave
-        long long tokens = std::max(even / 4, std::min<long long>(even, 512));
+        long long tokens = std::max(even / std::min(B, 4), std::min<long long>(even, 512));
         tokens = (std::min(tokens, see) + 127) / 128 * 128;
         p.S.tokens = (int)tokens;
         p.S.n_splits = (int)((see + tokens - 1) / tokens);

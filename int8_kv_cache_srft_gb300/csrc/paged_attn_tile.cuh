@@ -107,11 +107,11 @@ constexpr int kRegs = 96;
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 112;"); }
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
 
-// 16-byte chunk (8 consecutive inputs x0..) of row n of R_s as fp16 hi (and lo)
-template <int D, bool LO>
+// 16-byte chunk (8 consecutive inputs x0..) of row n of R_s times 2^UP as fp16 hi (and lo)
+template <int D, bool LO, int UP = 0>
 __device__ __forceinline__ void r_chunk(int n, int x0, bool srht, const float2* tw, const uint32_t* sg, uint4& hi,
                                         uint4& lo) {
-    const float isd = rsqrtf((float)D), c2 = 1.41421356237309505f * isd;
+    const float isd = rsqrtf((float)D) * (float)(1 << UP), c2 = 1.41421356237309505f * isd;
     uint32_t h[4], l[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -160,14 +160,29 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t w2, uint32_t sh, 
 template <int DP>
 struct Piece {
     uint32_t w[DP / 4];   // 8-bit: DP/4 words, 4-bit: the first DP/8
-    float sc[DP / 16];    // scale of each 16-coordinate unit
+    float sc[DP / 16];    // scale of each 16-coordinate unit, or (packed) its bits as loaded
+    bool packed;          // sc[0 .. 1] hold the units' fp16 scales two a word, sc[0] their e8m0 bytes: a conversion
+                          // beside the load would wait for it
 };
+template <int DP>
+__device__ __forceinline__ void unpack_scales(Piece<DP>& p, int sfmt) {
+    constexpr int U = DP / 16;
+    if (!p.packed) return;
+    const uint32_t a = __float_as_uint(p.sc[0]), b = U > 2 ? __float_as_uint(p.sc[U > 2 ? 1 : 0]) : 0u;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const uint32_t w = i < 2 ? a : b;
+        if (sfmt == SRFTKV_SCALE_FP16) p.sc[i] = __half2float(__ushort_as_half((unsigned short)(w >> (16 * (i & 1)))));
+        else p.sc[i] = __uint_as_float(((a >> (8 * i)) & 0xFFu) << 23);
+    }
+}
 
 // Load the piece of row `row` (packed row index, -1: zeros) that starts at coordinate x0
 template <int D, int DP>
 __device__ __forceinline__ void load_piece(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                            long long row, int x0, int bits, int sfmt, int lg_group, Piece<DP>& p) {
     constexpr int U = DP / 16;
+    p.packed = lg_group == 4 && sfmt != SRFTKV_SCALE_FP32;
     if (row < 0) {
 #pragma unroll
         for (int i = 0; i < DP / 4; ++i) p.w[i] = 0u;
@@ -203,24 +218,17 @@ __device__ __forceinline__ void load_piece(const uint8_t* __restrict__ codes, co
             }
         } else if (sfmt == SRFTKV_SCALE_FP16) {
             const __half* s = reinterpret_cast<const __half*>(scales) + row * ng + x0 / 16;
-            uint32_t v[U / 2];
             if constexpr (U == 4) {
                 const uint2 t = __ldg(reinterpret_cast<const uint2*>(s));
-                v[0] = t.x, v[1] = t.y;
+                p.sc[0] = __uint_as_float(t.x), p.sc[1] = __uint_as_float(t.y);
             } else {
-                v[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
-            }
-#pragma unroll
-            for (int i = 0; i < U / 2; ++i) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
-                p.sc[2 * i] = f.x, p.sc[2 * i + 1] = f.y;
+                p.sc[0] = __uint_as_float(__ldg(reinterpret_cast<const uint32_t*>(s)));
             }
         } else {
             uint32_t v;
             if constexpr (U == 4) v = __ldg(reinterpret_cast<const uint32_t*>(scales + row * ng + x0 / 16));
             else v = __ldg(reinterpret_cast<const unsigned short*>(scales + row * ng + x0 / 16));
-#pragma unroll
-            for (int i = 0; i < U; ++i) p.sc[i] = __uint_as_float(((v >> (8 * i)) & 0xFFu) << 23);
+            p.sc[0] = __uint_as_float(v);
         }
     } else {
 #pragma unroll
@@ -291,6 +299,8 @@ __global__ void __launch_bounds__(256) paged_expand_kernel(const __grid_constant
         tile::load_piece<D, DP>(P.kc, P.ks, row, x0, W.bits_k, P.sfmt, P.lg_group, pk);
         tile::load_piece<D, DP>(P.vc, P.vs, row, x0, W.bits_v, P.sfmt, P.lg_group, pv);
         const bool lo = P.sfmt == SRFTKV_SCALE_FP32;
+        tile::unpack_scales(pk, P.sfmt);
+        tile::unpack_scales(pv, P.sfmt);
         tile::store_piece_any<D, BN, DP>(smem, r, x0, W.bits_k, lo, pk);
         tile::store_piece_any<D, BN, DP>(smem + C::TB, r, x0, W.bits_v, lo, pv);
         ptx::fence_proxy_async_smem();
@@ -693,10 +703,15 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
         const int dt = threadIdx.x - 256, r = dt / PER, x0 = (dt % PER) * DP;
         const int* table = P.table + (long long)b * P.max_pages;
         const bool lo = P.sfmt == SRFTKV_SCALE_FP32;
-        auto row_of = [&](int t) -> long long {  // packed row of this thread's token in tile t, -1: none
+        // the page of this thread's token in tile t (looked up two tiles ahead, and not looked at until its row is wanted),
+        // and its packed row, -1: none
+        auto page_of = [&](int t) -> int {
+            const int tok = (ta + t) * BN + r;
+            return t < n && tok < len ? __ldg(table + (tok >> P.lg_page)) : 0;
+        };
+        auto row_of = [&](int t, int pg) -> long long {
             const int tok = (ta + t) * BN + r;
             if (t >= n || tok >= len) return -1;
-            const int pg = __ldg(table + (tok >> P.lg_page));
             if ((unsigned)pg >= (unsigned)P.n_pages) {
                 atomicOr(P.fault, kFaultPage);
                 return -1;
@@ -731,19 +746,23 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
             }
         } else {
         tile::Piece<DP> pk, pv;
-        long long row = row_of(0);
+        long long row = row_of(0, page_of(0));
         tile::load_piece<D, DP>(P.kc, P.ks, row, x0, W.bits_k, P.sfmt, P.lg_group, pk);
         tile::load_piece<D, DP>(P.vc, P.vs, row, x0, W.bits_v, P.sfmt, P.lg_group, pv);
-        row = row_of(1);
+        int next = page_of(1);
         for (int t = 0; t < n; ++t) {
+            row = row_of(t + 1, next);
+            next = page_of(t + 2);
             const int st = t & 1;
             if (t >= 2 && !wait(freed(S_DONE, t - 2), freed_parity(t - 2))) break;
+            tile::unpack_scales(pk, P.sfmt);
             tile::store_piece_any<D, BN, DP>(smem + C::OFF_K + st * C::TB, r, x0, W.bits_k, lo, pk);
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(k_bar(t)));
             tile::load_piece<D, DP>(P.kc, P.ks, row, x0, W.bits_k, P.sfmt, P.lg_group, pk);
             if (t >= 2 && !wait(freed(PV_DONE, t - 2), freed_parity(t - 2))) break;
+            tile::unpack_scales(pv, P.sfmt);
             tile::store_piece_any<D, BN, DP>(smem + C::OFF_V + st * C::TB, r, x0, W.bits_v, lo, pv);
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -752,7 +771,6 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                 if (no_next_k(t)) ptx::mbar_arrive(bar(v_bar(t)));
             }
             tile::load_piece<D, DP>(P.vc, P.vs, row, x0, W.bits_v, P.sfmt, P.lg_group, pv);
-            row = row_of(t + 2);
         }
         }
         if (W.n_parts == 1 && !failed) {

@@ -27,6 +27,10 @@ namespace srftkv {
 
 namespace ctc {
 
+// The write holds R_s times 2^8: its residual lo (2^-12 of entries near sqrt(2/d)) is then a normal fp16 number, and
+// P is good to about 2^-23 of the row; codes of 8 bits turn on 2^-20 of a group's largest value.
+constexpr int kUp = 8;
+
 template <int D, bool WRITE>
 struct Cfg {
     // Warps that bring tiles in, and that take them out: the heavier end of each direction gets sixteen (with eight at
@@ -80,10 +84,13 @@ __device__ __forceinline__ Tile tile_at(const PagedCodecParams& P, int u, int pe
     t.t0 = tb * 128;
     return t;
 }
-// token t's packed row in head h, or -1 (padding, outside the pool, past the call's tokens)
-__device__ __forceinline__ long long row_of(const PagedCodecParams& P, int t, int h) {
-    if (t >= P.n_tokens) return -1;
-    const long long slot = __ldg(P.slots + t);
+// Token t's slot as it stands in the list (-1 past the call's tokens).  Looked up a tile ahead and not looked at until
+// then: a check beside the load holds the warp for the load's latency, once a tile.
+__device__ __forceinline__ long long slot_of(const PagedCodecParams& P, int t) {
+    return t < P.n_tokens ? __ldg(P.slots + t) : -1;
+}
+// its packed row in head h, or -1 (padding, outside the pool)
+__device__ __forceinline__ long long row_of(const PagedCodecParams& P, long long slot, int h) {
     if (slot < 0) return -1;
     if (slot >= P.n_slots) {
         atomicOr(P.fault, kFaultSlot);
@@ -133,7 +140,7 @@ struct CtcCommon {
             const int r = c / (D / 8), ch = c % (D / 8);
             uint4 hi, lo;
             uint8_t* at = smem + (ch >> 3) * (ROWS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-            tile::r_chunk<D, WRITE>(WRITE ? n0 + r : dq_kperm(r), 8 * ch, srht, tw, sg, hi, lo);
+            tile::r_chunk<D, WRITE, WRITE ? ctc::kUp : 0>(WRITE ? n0 + r : dq_kperm(r), 8 * ch, srht, tw, sg, hi, lo);
             *reinterpret_cast<uint4*>(at) = hi;
             if constexpr (WRITE) *reinterpret_cast<uint4*>(at + ROWS * D * 2) = lo;
         }
@@ -255,13 +262,16 @@ __global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_
         // every other tile
         constexpr int UNITS = C::NB / 32, GROUPS = C::NE / 4 / UNITS;
         const int quarter = warp & 3, unit = ((warp - C::NL) >> 2) % UNITS, group = ((warp - C::NL) >> 2) / UNITS;
+        auto slot_at = [&](int u) { return u < total ? ctc::slot_of(P, ctc::tile_at(P, u, per_side).t0 + 32 * quarter + lane) : -1ll; };
         int i_tile = group;
+        long long next = slot_at(first + group * step);
         for (int u = first + group * step; u < total; u += GROUPS * step, i_tile += GROUPS) {
             const int a = i_tile % C::NACC;
             const ctc::Tile t = ctc::tile_at(P, u, per_side);
             const PagedSideK& sd = P.side[t.side];
             const int r = 32 * quarter + lane;
-            const long long row = ctc::row_of(P, t.t0 + r, t.h);
+            const long long row = ctc::row_of(P, next, t.h);
+            next = slot_at(u + GROUPS * step);
             if (!__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(S::ACC_FULL + a), (i_tile / C::NACC) & 1))) {
                 failed = true;
                 break;
@@ -296,8 +306,14 @@ __global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_
                     const int ng = D >> P.lg_group, sb = sd.sfmt == SRFTKV_SCALE_FP32 ? 4 : sd.sfmt == SRFTKV_SCALE_FP16 ? 2 : 1;
                     uint8_t* srow = sd.scales + (row * ng + (col >> P.lg_group)) * sb;
                     uint8_t* crow = sd.codes + row * (D * sd.bits / 8) + col * sd.bits / 8;
-                    if (sd.bits == 4) quant_store_row_any<32, 4>(z, P.group, sd.sfmt, crow, srow);
-                    else quant_store_row_any<32, 8>(z, P.group, sd.sfmt, crow, srow);
+                    auto put = [&](auto bits) {
+                        constexpr int B = decltype(bits)::value;
+                        if (sd.sfmt == SRFTKV_SCALE_FP32) quant_store_row<32, B, SRFTKV_SCALE_FP32, ctc::kUp>(z, P.group, crow, srow);
+                        else if (sd.sfmt == SRFTKV_SCALE_FP16) quant_store_row<32, B, SRFTKV_SCALE_FP16, ctc::kUp>(z, P.group, crow, srow);
+                        else quant_store_row<32, B, SRFTKV_SCALE_E8M0, ctc::kUp>(z, P.group, crow, srow);
+                    };
+                    if (sd.bits == 4) put(std::integral_constant<int, 4>{});
+                    else put(std::integral_constant<int, 8>{});
                 }
                 __syncwarp();
             }
@@ -316,11 +332,14 @@ __global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_
             tc::fence_after_sync();
             if (one) {
                 const uint32_t ao = tile::desc_k(sbase + C::OFF_A + s * C::A_BYTES), bo = tile::desc_k(sbase), dst = tmem + a * C::NB;
+                // lo first: an accumulation rounds to the size of the sum so far, which lo leaves small, so only the D/16
+                // steps of hi count
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t as = (ks >> 2) * 1024 + (ks & 3) * 2, bs = (ks >> 2) * (C::NB * 8) + (ks & 3) * 2;
-                    tc::mma_f16(dst, tile::desc(ao + as), tile::desc(bo + bs), tile::idesc(128, C::NB, false), ks > 0);
-                    tc::mma_f16(dst, tile::desc(ao + as), tile::desc(bo + bs + C::NB * D / 8), tile::idesc(128, C::NB, false), 1);
+                for (int ks = 0; ks < 2 * (D / 16); ++ks) {
+                    const int k = ks % (D / 16);
+                    const uint32_t as = (k >> 2) * 1024 + (k & 3) * 2, bs = (k >> 2) * (C::NB * 8) + (k & 3) * 2;
+                    tc::mma_f16(dst, tile::desc(ao + as), tile::desc(bo + bs + (ks < D / 16 ? C::NB * D / 8 : 0)),
+                                tile::idesc(128, C::NB, false), ks > 0);
                 }
                 tc::commit(bar(S::A_EMPTY + s));
                 tc::commit(bar(S::ACC_FULL + a));
@@ -357,15 +376,12 @@ __global__ void __launch_bounds__(ctc::Cfg<D, false>::THREADS, 1) paged_dequanti
         constexpr int DP = D / C::TPR, PD = C::PD, U = DP / 16;
         const int r = threadIdx.x / C::TPR, x0 = (threadIdx.x % C::TPR) * DP;
         tile::Piece<DP> p;
-        auto row_of = [&](int u) -> long long {
-            if (u >= total) return -1;
-            const ctc::Tile t = ctc::tile_at(P, u, per_side);
-            return ctc::row_of(P, t.t0 + r, t.h);
-        };
+        auto slot_at = [&](int u) { return u < total ? ctc::slot_of(P, ctc::tile_at(P, u, per_side).t0 + r) : -1ll; };
         const int ng = D >> P.lg_group;
         auto raw = [&](int q, int i) { return (uint32_t)(C::OFF_RAW + q * C::RAW + (i * C::NL * 32 + (int)threadIdx.x) * 16); };
-        auto load = [&](int u, int q, long long row) {  // into the raw ring (or registers)
+        auto load = [&](int u, int q, long long slot) {  // into the raw ring (or registers)
             if (u < total) {
+                const long long row = ctc::row_of(P, slot, ctc::tile_at(P, u, per_side).h);
                 const PagedSideK& sd = P.side[u >= per_side];
                 if constexpr (C::AHEAD) {
                     const int n = row < 0 ? 0 : 16;
@@ -412,17 +428,17 @@ __global__ void __launch_bounds__(ctc::Cfg<D, false>::THREADS, 1) paged_dequanti
             }
         };
 #pragma unroll
-        for (int j = 0; j < (C::AHEAD ? PD : 1); ++j) load(first + j * step, j, row_of(first + j * step));
+        for (int j = 0; j < (C::AHEAD ? PD : 1); ++j) load(first + j * step, j, slot_at(first + j * step));
         constexpr int NEXT = C::AHEAD ? PD : 1;
-        long long row = row_of(first + NEXT * step);
+        long long next = slot_at(first + NEXT * step);
         int i_tile = 0;
         for (int u = first; u < total; u += step, ++i_tile) {
             const int s = i_tile % C::ST, use = i_tile / C::ST;
             if constexpr (C::AHEAD) {
                 ctc::wait_copies<PD - 1>();
                 unload(u, i_tile % PD);
-                load(u + PD * step, i_tile % PD, row);  // (the pieces are this thread's own: read before they are replaced)
-                row = row_of(u + (PD + 1) * step);
+                load(u + PD * step, i_tile % PD, next);  // (the pieces are this thread's own: read before they are replaced)
+                next = slot_at(u + (PD + 1) * step);
             }
             if (use > 0 && !__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(S::A_EMPTY + s), (use - 1) & 1))) {
                 failed = true;
@@ -430,6 +446,7 @@ __global__ void __launch_bounds__(ctc::Cfg<D, false>::THREADS, 1) paged_dequanti
             }
             uint8_t* a = smem + C::OFF_A + s * C::A_BYTES;
             const PagedSideK& sd = P.side[u >= per_side];
+            if constexpr (!C::AHEAD) tile::unpack_scales(p, sd.sfmt);
             if (sd.lambda == nullptr) {
                 tile::store_piece_any<D, 128, DP>(a, r, x0, sd.bits, sd.sfmt == SRFTKV_SCALE_FP32, p);
             } else {
@@ -454,8 +471,8 @@ __global__ void __launch_bounds__(ctc::Cfg<D, false>::THREADS, 1) paged_dequanti
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(S::A_FULL + s));
             if constexpr (!C::AHEAD) {
-                load(u + step, 0, row);
-                row = row_of(u + 2 * step);
+                load(u + step, 0, next);
+                next = slot_at(u + 2 * step);
             }
         }
         if constexpr (C::AHEAD) ctc::wait_copies<0>();
@@ -464,19 +481,15 @@ __global__ void __launch_bounds__(ctc::Cfg<D, false>::THREADS, 1) paged_dequanti
         constexpr int GROUPS = C::NE / 8;
         const int quarter = warp & 3, c0 = (((warp - C::NL) >> 2) & 1) * (D / 2), group = (warp - C::NL) >> 3;
         uint8_t* stage = smem + C::OFF_OUT + (warp - C::NL) * 2048;
-        auto live_at = [&](int u) -> bool {
-            if (u >= total) return false;
-            const ctc::Tile t = ctc::tile_at(P, u, per_side);
-            return ctc::row_of(P, t.t0 + 32 * quarter + lane, t.h) >= 0;
-        };
+        auto slot_at = [&](int u) { return u < total ? ctc::slot_of(P, ctc::tile_at(P, u, per_side).t0 + 32 * quarter + lane) : -1ll; };
         int i_tile = group;
-        bool next = live_at(first + group * step);  // (its slot is looked up a tile ahead)
+        long long next = slot_at(first + group * step);
         for (int u = first + group * step; u < total; u += GROUPS * step, i_tile += GROUPS) {
             const int a = i_tile % C::NACC;
             const ctc::Tile t = ctc::tile_at(P, u, per_side);
             const PagedSideK& sd = P.side[t.side];
-            const uint32_t rows = __ballot_sync(0xffffffffu, next);
-            next = live_at(u + GROUPS * step);
+            const uint32_t rows = __ballot_sync(0xffffffffu, ctc::row_of(P, next, t.h) >= 0);
+            next = slot_at(u + GROUPS * step);
             // this lane's place in the coalesced stores: 16-byte piece lane % 4 of rows lane / 4 + 8 j
             uint16_t* x = static_cast<uint16_t*>(sd.x) + (long long)(t.t0 + 32 * quarter + (lane >> 2)) * sd.x_stride +
                           (long long)t.h * D + c0 + 8 * (lane & 3);
