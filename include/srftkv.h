@@ -371,17 +371,23 @@ typedef struct srftkv_paged_batch {
  *   k, v   : both sides, sharing all sizes and the scale format
  *   sm_scale: <= 0 selects 1/sqrt(d)
  *   workspace: device scratch of q4kv_paged_attention_workspace_size(...)
- *            bytes, 16-byte aligned, uninitialised; calls that may run at the
- *            same time need one each
+ *            bytes, 16-byte aligned, uninitialised (NULL where that is 0); calls
+ *            that may run at the same time need one each, also the replays of two
+ *            captured graphs.  It holds partial results and, for prompts of many
+ *            rows, up to 1 GiB of tiles
  * seq_lens[b] is clamped to [0, min(max_seq_len, max_pages * page_size)] and a
  * sequence's query count to max_q (rows past it are left as they were).  A
  * block-table entry outside [0, n_pages) reads no memory outside the pools: its
- * tokens count as rows of zeros and bit 17 of the fault word is set.
+ * tokens count as rows of zeros and bit 17 of the fault word is set.  Entries of
+ * pages that no query of the sequence sees (before every window) may be stale.
  * Requires Hq % H == 0, Hq / H <= 128, total_q * Hq < 2^31, max_q * Hq / H <=
  * 2^22, B * H <= 65535.
- * Values code * scale (lambda times the rotated row) are formed in fp16 where
- * they enter the tensor cores: they must stay below 65504 in size, and those
- * below 2^-14 keep fewer than 11 bits.
+ * Values code * scale (lambda times the rotated row), bf16 queries, the rotated
+ * queries times sm_scale log2(e) / lambda_K, and the results are formed in fp16
+ * where they enter the tensor cores: they must stay below 65504 in size, and
+ * those below 2^-14 keep fewer than 11 bits.  Cached tokens must be finite: a
+ * token with a scale that is not makes NaN also of rows of the same call that
+ * mask it, where they share a tile of 128 tokens with it.
  */
 int q4kv_paged_attention(const void* q, int64_t q_stride, void* out, int64_t out_stride, int dtype, int Hq,
                          const srftkv_pages* k, const srftkv_pages* v, const srftkv_paged_batch* batch, float sm_scale,

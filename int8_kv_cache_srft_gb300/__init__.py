@@ -237,7 +237,8 @@ class Pages:
     transform: str = "srft"          # "srft" or "srht"
     scale_format: str = "fp32"       # "fp32", "fp16" or "e8m0"
 
-    # The marshalled struct is built (and the tensors checked) once and reused until a field is assigned again.
+    # The marshalled struct is built (and the tensors checked) once and reused until a field is assigned again (a
+    # tensor changed in place keeps its address; one resized or replaced must be assigned anew).
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         if name != "_c":
@@ -277,7 +278,8 @@ def alloc_pages(n_pages: int, page_size: int, H: int, d: int, bits: int, group: 
 @dataclass
 class PagedBatch:
     """The sequences of an attention call (srftkv_paged_batch in include/srftkv.h).  The tensors stay where they
-    are and may change in place between calls, within total_q, max_q and max_seq_len."""
+    are and may change in place between calls, within total_q, max_q and max_seq_len (one resized or replaced must
+    be assigned anew)."""
 
     block_table: torch.Tensor       # int32 [B][max_pages]
     seq_lens: torch.Tensor          # int32 [B]
@@ -331,6 +333,8 @@ def _paged_device(fn: str, pages: Pages, stream):
     """The pools' device, which has to be the current one, and the stream of the call."""
     dev = pages.codes.device
     if dev.type != "cuda":
+        if torch.cuda.is_available():
+            _invalid(fn, f"the pools must be CUDA tensors, not on {dev}")
         return dev, None
     now = torch.cuda.current_device()
     if dev.index != now:
@@ -342,6 +346,8 @@ def _paged_codec(fn: str, k: Pages | None, xk, v: Pages | None, xv, slots: torch
     side = k if k is not None else v
     if side is None:
         _invalid(fn, "at least one of k, v must be given")
+    if (k is not None and xk is None) or (v is not None and xv is None):
+        _invalid(fn, "each side that is given needs its rows")
     dev, stream = _paged_device(fn, side, stream)
     if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous() or slots.device != dev:
         _invalid(fn, "slots must be a contiguous int64 [n_tokens] on the pools' device")
@@ -376,8 +382,9 @@ def q4kv_paged_attention_workspace_size(k: Pages, Hq: int, batch: PagedBatch, wi
 
 
 def q4kv_paged_attention(q: torch.Tensor, out: torch.Tensor, k: Pages, v: Pages, batch: PagedBatch, sm_scale: float,
-                         window: int, sign_seed: int, workspace: torch.Tensor, stream=None) -> None:
-    """Causal attention of the query rows q [total_q][Hq][d] over the pages; out like q (see include/srftkv.h)."""
+                         window: int, sign_seed: int, workspace: torch.Tensor | None, stream=None) -> None:
+    """Causal attention of the query rows q [total_q][Hq][d] over the pages; out like q (see include/srftkv.h).
+    workspace: at least q4kv_paged_attention_workspace_size(...) bytes; None where that is 0."""
     fn = "q4kv_paged_attention"
     dev, stream = _paged_device(fn, k, stream)
     if q.dtype not in DTYPES or q.dim() != 3:
@@ -386,11 +393,12 @@ def q4kv_paged_attention(q: torch.Tensor, out: torch.Tensor, k: Pages, v: Pages,
     n, Hq = b.contents.total_q, q.shape[1]
     qs = _rows_arg(fn, "q", q, n, Hq, k.d, q.dtype, dev)
     os = _rows_arg(fn, "out", out, n, Hq, k.d, q.dtype, dev)
-    if batch.block_table.device != dev or v.codes.device != dev or workspace.device != dev:
+    if batch.block_table.device != dev or v.codes.device != dev or (
+            workspace is not None and (workspace.device != dev or not workspace.is_contiguous())):
         _invalid(fn, "the pools, the batch's tables and the workspace must be on one device")
     rc = library().q4kv_paged_attention(q.data_ptr(), qs, out.data_ptr(), os, DTYPES[q.dtype], Hq, k.c_pointer(),
-                                        v.c_pointer(), b, sm_scale, window, sign_seed, workspace.data_ptr(),
-                                        workspace.nbytes, stream)
+                                        v.c_pointer(), b, sm_scale, window, sign_seed, _ptr(workspace),
+                                        workspace.nbytes if workspace is not None else 0, stream)
     if rc:
         _check(fn, rc)
 

@@ -117,6 +117,8 @@ static int check_batch(const char* fn, const srftkv_pages* k, int Hq, const srft
     if ((long long)b->B * k->H > 65535) return bad(fn, "B * H must be at most 65535");
     return SRFTKV_OK;
 }
+// A window of all positions is none
+static int window_of(int window, int max_len) { return window < max_len ? window : 0; }
 static int batch_len(const srftkv_pages* k, const srftkv_paged_batch* b) {
     return b->max_seq_len ? b->max_seq_len : b->max_pages * k->page_size;
 }
@@ -145,7 +147,8 @@ size_t q4kv_paged_attention_workspace_size(const srftkv_pages* k, int Hq, const 
     const char* fn = "q4kv_paged_attention_workspace_size";
     if (!k || !b) return 0;
     if (check_pages(fn, k) || check_batch(fn, k, Hq, b) || window < 0) return 0;
-    return paged_attention_workspace(k->d, Hq, k->H, b->B, b->total_q, b->max_q, batch_len(k, b), window);
+    const int len = batch_len(k, b);
+    return paged_attention_workspace(k->d, Hq, k->H, b->B, b->total_q, b->max_q, len, window_of(window, len));
 }
 
 int q4kv_paged_attention(const void* q, int64_t q_stride, void* out, int64_t out_stride, int dtype, int Hq,
@@ -206,7 +209,7 @@ int q4kv_paged_attention(const void* q, int64_t q_stride, void* out, int64_t out
     P.sfmt = k->scale_format;
     P.tr_k = k->transform;
     P.tr_v = v->transform;
-    P.window = window;
+    P.window = window_of(window, P.max_len);
     const float sc = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt((float)k->d);
     P.qscale = sc * 1.4426950408889634f;
     sign_masks(k->d, sign_seed, P.sign_mask);
@@ -217,7 +220,7 @@ int q4kv_paged_attention(const void* q, int64_t q_stride, void* out, int64_t out
     c.workspace = workspace;
     c.workspace_bytes = workspace_bytes;
     c.stream = static_cast<cudaStream_t>(stream);
-    const size_t need = paged_attention_workspace(k->d, Hq, k->H, P.B, P.total_q, P.max_q, P.max_len, window);
+    const size_t need = paged_attention_workspace(k->d, Hq, k->H, P.B, P.total_q, P.max_q, P.max_len, P.window);
     if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) {
         set_error("%s: workspace must be 16-byte aligned and hold %zu bytes (got %zu)", fn, need, workspace_bytes);
         return SRFTKV_ERR_INVALID;

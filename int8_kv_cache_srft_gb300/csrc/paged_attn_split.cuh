@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(128, D == 256 ? 2 : 3)
         const int i = (row0 + r) / P.rep;
         return (q0 + i) * stride + (long long)(h * P.rep + (row0 + r - i * P.rep)) * D;
     };
-    const int first_chunk = P.window ? max(0, pos_lo - P.window + 1) / CH : 0;
+    const int low_all = P.window ? max(0, pos_lo - P.window + 1) : 0;  // the first token any row sees
+    const int first_chunk = low_all / CH;
     const int c_begin = first_chunk + spl * W.chunks;
     const int c_end = min(pos_hi >= 0 ? pos_hi / CH + 1 : 0, c_begin + W.chunks);
     if (c_begin >= c_end) {  // nothing visible here: zeros, or empty partials
@@ -248,9 +249,10 @@ __global__ void __launch_bounds__(128, D == 256 ? 2 : 3)
             int have[NT];       // tokens of the 16 that are there
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
-                const bool ok = (unsigned)pages[x] < (unsigned)P.n_pages;
+                const bool seen = t0 + 16 * x + 15 >= low_all;  // (pages before every window may be gone)
+                const bool ok = seen && (unsigned)pages[x] < (unsigned)P.n_pages;
                 have[x] = ok ? len - t0 - 16 * x : 0;
-                if (!ok) atomicOr(P.fault, kFaultPage);
+                if (seen && !ok) atomicOr(P.fault, kFaultPage);
                 row[x] = ok ? (long long)(pages[x] * P.Hkv + h) << P.lg_page | ((t0 + 16 * x) & ((1 << P.lg_page) - 1)) : 0;
             }
             auto codes = [&](const uint8_t* plane, uint32_t dst, auto pl, auto rbc) {

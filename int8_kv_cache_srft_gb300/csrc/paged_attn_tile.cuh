@@ -284,11 +284,11 @@ __global__ void __launch_bounds__(256) paged_expand_kernel(const __grid_constant
     const int t = blockIdx.x, b = blockIdx.y / P.Hkv, h = blockIdx.y - b * P.Hkv;
     const int len = min(max(P.seq_lens[b], 0), P.max_len);
     const int m_tok = P.cu_q ? min(max(P.cu_q[b + 1] - P.cu_q[b], 0), P.max_q) : 1;
-    const int low = P.window ? len - m_tok - P.window + 1 : 0;  // the first token the first query sees
-    if (t * BN < len && (t + 1) * BN > low) {
+    const int low = P.window ? max(0, len - m_tok - P.window + 1) : 0;  // the first token the first query sees
+    if (m_tok > 0 && t * BN < len && (t + 1) * BN > low) {
         const int r = threadIdx.x / PER, x0 = (threadIdx.x % PER) * DP, tok = t * BN + r;
         long long row = -1;
-        if (tok < len) {
+        if (tok < len && tok >= low) {  // (pages before every window may be gone: not looked at)
             const int pg = __ldg(P.table + (long long)b * P.max_pages + (tok >> P.lg_page));
             if ((unsigned)pg < (unsigned)P.n_pages)
                 row = (((long long)pg * P.Hkv + h) << P.lg_page) | (tok & ((1 << P.lg_page) - 1));
@@ -338,11 +338,15 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
     m_tok = min(m_tok, P.total_q - q0);
     const int n_rows = m_tok * P.rep;
     const int row0 = blk * W.rows_per_block;
-    if (row0 >= n_rows) return;
+    if (row0 >= n_rows) {
+        griddep_wait();  // (a kernel after this one may start only once the expanding kernel is over too)
+        return;
+    }
     const int len = min(max(P.seq_lens[b], 0), P.max_len);
     const int rows_here = min(W.rows_per_block, n_rows - row0);
     const int pos_lo = len - m_tok + row0 / P.rep, pos_hi = len - m_tok + (row0 + rows_here - 1) / P.rep;
-    int ta = P.window ? max(0, pos_lo - P.window + 1) / BN : 0;
+    const int low = P.window ? max(0, pos_lo - P.window + 1) : 0;  // the first token any row sees
+    int ta = low / BN;
     int tb = pos_hi >= 0 ? pos_hi / BN + 1 : 0;
     ta = ta + split * W.tps;
     tb = min(tb, W.n_splits > 1 ? ta + W.tps : tb);
@@ -356,6 +360,7 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
         i += q0;
     };
     if (n == 0) {  // nothing visible: zeros, or empty partials
+        griddep_wait();
         for (int r = threadIdx.x; r < rows_here; r += blockDim.x) {
             int i, hq;
             out_row(r, i, hq);
@@ -711,7 +716,7 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
         };
         auto row_of = [&](int t, int pg) -> long long {
             const int tok = (ta + t) * BN + r;
-            if (t >= n || tok >= len) return -1;
+            if (t >= n || tok >= len || tok < low) return -1;  // (pages before every window may be gone)
             if ((unsigned)pg >= (unsigned)P.n_pages) {
                 atomicOr(P.fault, kFaultPage);
                 return -1;

@@ -1,6 +1,10 @@
 """The paged cache against its definition in 64 bits: rows written into slots
 and read back, and attention of ragged query rows over the pages."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -329,6 +333,104 @@ def test_bad_pages_read_nothing_and_are_reported(m):
     R.check(out, ref, tol)
 
 
+@pytest.mark.parametrize("d,m", [(128, 1), (128, 5), (128, 70), (128, 160), (64, 160), (256, 100)])
+def test_pages_before_every_window_may_be_gone(d, m):
+    """Entries of pages that no query sees are not looked at: nothing is reported, the answer is the same bits."""
+    window, lens = 40, [700, 333]
+    c = R.Cache(K, lens, 2, d, 4, 4, 16, "fp16", 16, BF16)
+    q = rand(2 * m, 8, d, dtype=BF16, seed=2)
+    b = c.batch(K, [m, m])
+    want = R.attend(K, c, q, b, window=window)
+    ref, tol = R.attention64(q, *c.sides, c.table.cpu().numpy(), lens, [m, m], c.seed, BF16, window)
+    R.check(want, ref, tol)
+    for s, n in enumerate(lens):
+        c.table[s, :max(0, n - m - window + 1) // 16] = -1
+    assert torch.equal(R.attend(K, c, q, b, window=window), want)
+    assert K.srftkv_device_fault() == 0
+
+
+@pytest.mark.parametrize("d,m", [(128, 170), (64, 170), (256, 110)])
+def test_bad_pages_of_long_prompts(d, m):
+    """The same where the tiles are laid down before (three row blocks and more)."""
+    c = R.Cache(K, [400, 180], 1, d, 4, 8, 16, "e8m0", 32, HALF)
+    c.table[0, 3], c.table[0, 7] = 1 << 28, -1
+    q = rand(2 * m, 4, d, dtype=HALF, seed=2)
+    out = R.attend(K, c, q, c.batch(K, [m, m]))
+    assert K.srftkv_device_fault() == 1 << 17
+    used = set(c.table.flatten().tolist())
+    zero = next(p for p in range(c.sides[0].codes.shape[0]) if p not in used)
+    for p in c.sides:
+        p.codes[zero], p.scales[zero] = 0, 0
+    c.table[0, 3] = c.table[0, 7] = zero
+    ref, tol = R.attention64(q, *c.sides, c.table.cpu().numpy(), [400, 180], [m, m], c.seed, HALF)
+    R.check(out, ref, tol)
+
+
+@pytest.mark.parametrize("m", [1, 4, 40, 300])
+def test_a_window_of_everything_and_rows_that_see_nothing(m):
+    """The largest window equals none, with more query rows than tokens too; a sequence without queries beside it."""
+    lens, qlens = [200, 2, 90], [m, m, 0]
+    c = R.Cache(K, lens, 1, 128, 8, 8, 16, "fp32", 64, HALF, transform="srft", transform_v="srht", lam=True)
+    q = rand(2 * m, 4, 128, dtype=HALF, seed=2)
+    b = c.batch(K, qlens)
+    want = R.attend(K, c, q, b)
+    ref, tol = R.attention64(q, *c.sides, c.table.cpu().numpy(), lens, qlens, c.seed, HALF)
+    R.check(want, ref, tol)
+    for window in (200, 2**31 - 1):
+        assert torch.equal(R.attend(K, c, q, b, window=window), want)
+    # and a call of three row blocks none of whose sequences has a query
+    b.cu_q.zero_()
+    out = torch.full_like(q, 3.0)
+    R.attend(K, c, q, b, out=out)
+    assert (out == 3).all()
+
+
+@pytest.mark.parametrize("n", [40, 2500, 12000])
+@pytest.mark.parametrize("tr,trv", [("srft", "srht"), ("srht", "srft")])
+def test_sides_with_different_transforms(n, tr, trv):
+    """bf16 rows of sizes from 2^-30 to 2^30 beside each other, K and V rotated differently; fp32 scales."""
+    p = [K.alloc_pages(-(-n // 32), 32, 1, 128, 8, 16, transform=t) for t in (tr, trv)]
+    size = torch.exp2(torch.arange(n, device="cuda") % 61 - 30.0)[:, None, None]
+    x = [(torch.randn(n, 1, 128, device="cuda", generator=torch.Generator("cuda").manual_seed(s)) * size).bfloat16()
+         for s in (1, 2)]
+    slots = torch.randperm(n, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    K.srft_kv_quantize_paged(p[0], x[0], p[1], x[1], slots, 9)
+    for a, side, t in zip(x, p, (tr, trv)):
+        z = O.rotate(R.f64(a), 9, t)
+        held = R.held_rows(side, slots.tolist())
+        # at most half a step of the group's scale, one eighth of a percent of it for the fp32 arithmetic
+        step = np.repeat(np.abs(z).reshape(n, 1, 8, 16).max(-1) / 127, 16, axis=-1)
+        assert (np.abs(held - z) <= 0.50125 * step).all()
+
+
+def test_refusals_on_the_gpu():
+    c = R.Cache(K, [500], 1, 128, 4, 4, 16, "fp16", 16, HALF)
+    k, v = c.sides
+    q, b = rand(1, 4, 128, dtype=HALF), c.batch(K)
+    out = torch.full_like(q, 2.0)
+    need = K.q4kv_paged_attention_workspace_size(k, 4, b)
+    assert need > 0
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+    cpu = K.Pages(k.codes.cpu(), k.scales.cpu(), 4, 128, 16, scale_format="fp16")
+    for call in (lambda: K.q4kv_paged_attention(q, out, k, v, b, 0.0, 0, 1, ws[:need - 16]),
+                 lambda: K.q4kv_paged_attention(q, out, k, v, b, 0.0, 0, 1, None),
+                 lambda: K.q4kv_paged_attention(q, out, k, v, b, 0.0, 0, 1, ws[8:]),
+                 lambda: K.q4kv_paged_attention(q, out, k, v, b, 0.0, 0, 1, ws.cpu()),
+                 lambda: K.q4kv_paged_attention(q, out, cpu, cpu, b, 0.0, 0, 1, ws),
+                 lambda: K.q4kv_paged_attention(q, out, k, cpu, b, 0.0, 0, 1, ws),
+                 lambda: K.srft_kv_quantize_paged(cpu, q[:, :1].cpu(), None, None, c.slots[:1].cpu(), 1),
+                 lambda: K.srft_kv_quantize_paged(k, q[:, :1], None, None, c.slots[:1].cpu(), 1),
+                 lambda: K.srft_kv_quantize_paged(k, None, v, q[:, :1], c.slots[:1], 1)):
+        with pytest.raises(K.SrftKvError) as e:
+            call()
+        assert e.value.code == K.SRFTKV_ERR_INVALID
+    assert (out == 2).all()
+    one = c.batch(K, max_seq_len=100)  # one split: no workspace
+    assert K.q4kv_paged_attention_workspace_size(k, 4, one) == 0
+    K.q4kv_paged_attention(q, out, k, v, one, 0.0, 0, 1, None)
+    assert torch.isfinite(out).all()
+
+
 @pytest.mark.parametrize("m", [1, 4, 80])
 @pytest.mark.parametrize("fmt", ["fp32", "fp16", "e8m0"])
 def test_ranges_of_the_scales(m, fmt):
@@ -374,7 +476,7 @@ def test_a_conversation():
         assert np.all(np.abs(R.f64(got) - want) <= R.dequant_tolerance(z, 1.0, want, BF16))
 
 
-@pytest.mark.parametrize("m,rep", [(1, 4), (5, 4), (90, 4)])
+@pytest.mark.parametrize("m,rep", [(1, 4), (5, 4), (90, 4), (160, 4)])
 def test_captured_and_replayed(m, rep):
     """A captured step (write, then attention) replayed with other rows, lengths and tables equals the eager calls
     bit for bit; two runs of one call are the same bits."""
@@ -410,6 +512,39 @@ def test_captured_and_replayed(m, rep):
         assert torch.equal(got, out)
         step()
         assert torch.equal(got, out)
+
+
+FIRST_CALLS = """
+import torch, int8_kv_cache_srft_gb300 as K
+k, v = [K.alloc_pages(64, 16, 2, 128, 4, 16) for _ in range(2)]
+for p in (k, v):
+    p.codes.fill_(0x11), p.scales.fill_(0.5)
+table = torch.arange(64, dtype=torch.int32, device="cuda").view(1, 64)
+for m in (1, 6, 40, 200):
+    cu = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+    b = K.PagedBatch(table, torch.tensor([900], dtype=torch.int32, device="cuda"), cu, total_q=m, max_q=m)
+    q, x = torch.randn(m, 8, 128, device="cuda").half(), torch.randn(m, 2, 128, device="cuda").half()
+    out, slots = torch.empty_like(q), torch.arange(900 - m, 900, device="cuda")
+    ws = torch.empty(max(16, K.q4kv_paged_attention_workspace_size(k, 8, b)), dtype=torch.uint8, device="cuda")
+    def step():
+        K.srft_kv_quantize_paged(k, x, v, x, slots, 1)
+        K.q4kv_paged_attention(q, out, k, v, b, 0.0, 0, 1, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    graph.replay()
+    got = out.clone()
+    step()
+    assert torch.equal(got, out), m
+assert K.srftkv_device_fault() == 0
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_two_streams_at_once():

@@ -126,3 +126,5 @@ def test_binding_checks_tensors():
         assert e.value.code == K.SRFTKV_ERR_INVALID
     with pytest.raises(K.SrftKvError):
         K.q4kv_paged_attention(x.float(), x, p, p, K.PagedBatch(t, n), 0.0, 0, 1, c)
+    with pytest.raises(K.SrftKvError):  # a side without its rows
+        K.srft_kv_quantize_paged(p, None, None, None, slots, 1)
