@@ -17,7 +17,10 @@
 // [2^-6, 2^15), else multiplied by the power of two that brings it to [1, 2); the
 // epilogue multiplies it back in.
 //
-// What bounds it: the bytes of x (2 d a vector) and of the rows (d b / 8 + scales).
+// What bounds it: the bytes of x (2 d a vector) and of the rows (d b / 8 + scales),
+// and near it the instructions of both ends (issue 58 % busy writing, 43 % reading).
+// 2 M rows at d = 128, 4-bit codes: written in 130 us from fp16 (5.7 TB/s, 84 % of the
+// copy rate), 197 from bf16, read back in 180 (4.0 TB/s); d = 64: 75, 108 and 115.
 #pragma once
 
 #include "codec_impl.cuh"
