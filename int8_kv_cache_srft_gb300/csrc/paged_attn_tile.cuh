@@ -118,29 +118,34 @@ constexpr int kRegs = 96;
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 112;"); }
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
 
-// 16-byte chunk (8 consecutive inputs x0..) of row n of R_s times 2^UP as fp16 hi (and lo)
+// Entries x0 .. x0 + 7 of row n of R_s times 2^UP
+template <int D, int UP>
+__device__ __forceinline__ void r_entries(int n, int x0, bool srht, const float2* tw, const uint32_t* sg, float (&v)[8]) {
+    const float isd = rsqrtf((float)D) * (float)(1 << UP), c2 = 1.41421356237309505f * isd;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int x = x0 + e;
+        if (srht) v[e] = (__popc(n & x) & 1) ? -isd : isd;
+        else if (n == 0) v[e] = isd;
+        else if (n == 1) v[e] = (x & 1) ? -isd : isd;
+        else {
+            const float2 w = tw[((n >> 1) * x) & (D - 1)];
+            v[e] = c2 * ((n & 1) ? w.y : w.x);
+        }
+        if (sg[x >> 1] & ((e & 1) ? 0x80000000u : 0x8000u)) v[e] = -v[e];
+    }
+}
+// the 16-byte chunk of them as fp16 hi (and lo)
 template <int D, bool LO, int UP = 0>
 __device__ __forceinline__ void r_chunk(int n, int x0, bool srht, const float2* tw, const uint32_t* sg, uint4& hi,
                                         uint4& lo) {
-    const float isd = rsqrtf((float)D) * (float)(1 << UP), c2 = 1.41421356237309505f * isd;
+    float v[8];
+    r_entries<D, UP>(n, x0, srht, tw, sg, v);
     uint32_t h[4], l[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        float v[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int x = x0 + 2 * j + e;
-            if (srht) v[e] = (__popc(n & x) & 1) ? -isd : isd;
-            else if (n == 0) v[e] = isd;
-            else if (n == 1) v[e] = (x & 1) ? -isd : isd;
-            else {
-                const float2 w = tw[((n >> 1) * x) & (D - 1)];
-                v[e] = c2 * ((n & 1) ? w.y : w.x);
-            }
-            if (sg[x >> 1] & (e ? 0x80000000u : 0x8000u)) v[e] = -v[e];
-        }
-        if constexpr (LO) split_pair_h2(v[0], v[1], h[j], l[j]);
-        else h[j] = pack_half2(v[0], v[1]);
+        if constexpr (LO) split_pair_h2(v[2 * j], v[2 * j + 1], h[j], l[j]);
+        else h[j] = pack_half2(v[2 * j], v[2 * j + 1]);
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     if constexpr (LO) lo = make_uint4(l[0], l[1], l[2], l[3]);

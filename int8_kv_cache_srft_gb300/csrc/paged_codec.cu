@@ -170,12 +170,12 @@ static int launch(const PagedCodecCall& c, bool quantize) {
     P.div_mul = div.mul;
     P.div_shift = div.shift;
     // Many rows: the tensor cores, which every CTA first builds R_s for (10 us a call at d = 128, 6 at 64, 19 to 30 at
-    // 256); few: one warp a row (d = 128: 8.8 us at 8192 rows, 14.3 at 16384; d = 64: 5.9 and 9.4; d = 256: 20 and 36
-    // at 16384 and 32768).  The write's epilogue holds 32 columns a thread, so its groups end there; both sides rotate
+    // 256); few: one warp a row (d = 128: 8.8 us at 8192 rows, 14.3 at 16384 against 10 here; d = 64: 5.9 and 9.4 against
+    // 5.6; d = 256: 20 and 36 at 16384 and 32768, against 25 at both written and 34 read back).  The write's epilogue holds 32 columns a thread, so its groups end there; both sides rotate
     // with one R_s.
     const long long rows = (long long)P.n_tokens * P.H * P.n_sides;
     const bool one_r = P.n_sides == 1 || P.side[0].transform == P.side[1].transform;
-    if (rows >= (c.d == 256 ? 20480 : 10240) && one_r && (!quantize || P.group <= 32)) {
+    if (rows >= (c.d < 256 ? 10240 : quantize ? 20480 : 28672) && one_r && (!quantize || P.group <= 32)) {
         if (c.d == 64) return launch_paged_codec_tc64(P, c.dtype, quantize, c.stream);
         if (c.d == 128) return launch_paged_codec_tc128(P, c.dtype, quantize, c.stream);
         return launch_paged_codec_tc256(P, c.dtype, quantize, c.stream);

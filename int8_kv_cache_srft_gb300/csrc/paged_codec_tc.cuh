@@ -4,8 +4,9 @@
 // tokens of one (side, head); the heads of a token block are neighbouring
 // tiles, so the SMs read and write whole tokens of x together.
 //
-//   write:  P = X . R_s^T (R_s as fp16 hi + lo, X exact), then lambda, group
-//           scales, rounding and packing, one thread a row and 32 columns
+//   write:  P = X . R_s^T (X exact; R_s as fp16 hi + lo beside fp16 rows, as three
+//           bf16 parts beside bf16 rows), then lambda, group scales, rounding and
+//           packing, one thread a row and 32 columns
 //   read:   X = P . R_s, P = code * scale / lambda rounded to fp16 once
 //
 // Warps (8 and 16, or 16 and 8): some bring a tile in (write: 16-bit rows,
@@ -13,14 +14,15 @@
 // A operand; the last issues the MMAs into a ring of accumulators; the others take
 // them out.
 //
-// bf16 rows go over to fp16 as they are where their largest value lies in
-// [2^-6, 2^15), else multiplied by the power of two that brings it to [1, 2); the
-// epilogue multiplies it back in.
+// At d = 256 three parts of R_s do not fit: there bf16 rows go over to fp16, as
+// they are where their largest value lies in [2^-6, 2^15), else multiplied by the
+// power of two that brings it to [1, 2); the epilogue multiplies it back in.
 //
 // What bounds it: the bytes of x (2 d a vector) and of the rows (d b / 8 + scales),
 // and near it the instructions of both ends (issue 58 % busy writing, 43 % reading).
 // 2 M rows at d = 128, 4-bit codes: written in 130 us from fp16 (5.7 TB/s, 84 % of the
-// copy rate), 197 from bf16, read back in 180 (4.0 TB/s); d = 64: 75, 108 and 115.
+// copy rate), 138 from bf16, read back in 180 (4.0 TB/s); d = 64: 75, 74 and 115.
+// 1 M rows at d = 256: 293, 372 (converted rows) and 230.
 #pragma once
 
 #include "codec_impl.cuh"
@@ -34,20 +36,24 @@ namespace ctc {
 // P is good to about 2^-23 of the row; codes of 8 bits turn on 2^-20 of a group's largest value.
 constexpr int kUp = 8;
 
-template <int D, bool WRITE>
+template <int D, bool WRITE, int DT>
 struct Cfg {
+    // rows of bf16 against three bf16 parts of R_s (24 bits), nothing to convert (d = 128, 2 M rows: 197 us converted)
+    static constexpr bool BF = WRITE && DT == SRFTKV_DTYPE_BF16 && D <= 128;
+    static constexpr int PARTS = !WRITE ? 1 : BF ? 3 : 2, UP = WRITE && !BF ? kUp : 0;
     // Warps that bring tiles in, and that take them out: the heavier end of each direction gets sixteen (with eight at
-    // both ends a tile took 2 us of dependent instructions, whatever the memory did)
-    static constexpr int NL = WRITE || D < 256 ? 8 : 16, NE = WRITE || D < 256 ? 16 : 8, THREADS = (NL + NE + 1) * 32, MMA = NL + NE;
+    // both ends a tile took 2 us of dependent instructions, whatever the memory did); but for the write at d = 256,
+    // where a tile waits in the loaders' registers and 25 warps leave too few
+    static constexpr int NL = WRITE || D < 256 ? 8 : 16, NE = D < 256 ? 16 : 8, THREADS = (NL + NE + 1) * 32, MMA = NL + NE;
     static constexpr int NB = WRITE && D == 256 ? 128 : D;  // output columns a CTA (d = 256: half of them)
     static constexpr int NSPLIT = D / NB;
-    static constexpr int B_BYTES = NB * D * 2 * (WRITE ? 2 : 1);
+    static constexpr int B_BYTES = NB * D * 2 * PARTS;
     static constexpr int A_BYTES = 128 * D * 2;
     // A stages.  d <= 128: the write's copies land in them PD tiles ahead; the read's raw bytes wait in a ring of
     // their own, PD tiles ahead, 16 bytes a thread and step.  d = 256 has room for one stage, and a tile waits in
     // registers.
     static constexpr bool AHEAD = D <= 128;
-    static constexpr int ST = !AHEAD ? 1 : WRITE ? 4 : 3, PD = 2;
+    static constexpr int ST = !AHEAD ? 1 : WRITE && !(BF && D == 128) ? 4 : 3, PD = 2;
     static constexpr int NACC = WRITE || D < 256 ? 4 : 2;       // accumulators of NB columns
     static constexpr int TPR = NL / 4;                          // read: threads a row
     static constexpr int RAW16 = D / (16 * TPR) + 1;            // 16-byte pieces a thread (8-bit codes; scales last)
@@ -56,8 +62,8 @@ struct Cfg {
     static constexpr int OFF_RAW = OFF_A + ST * A_BYTES;
     static constexpr int OFF_TW = OFF_RAW + PD * RAW;
     static constexpr int OFF_SG = OFF_TW + D * 8;
-    static constexpr int OFF_RF = OFF_SG + D * 2;      // write: 2^e of the rows of eight tiles
-    static constexpr int OFF_OUT = OFF_RF + (WRITE ? 8 * 128 * 4 : 0);  // read: 32 rows of 64 bytes for each epilogue warp
+    static constexpr int OFF_RF = OFF_SG + D * 2;      // write of converted bf16 rows: 2^e of the rows of eight tiles
+    static constexpr int OFF_OUT = OFF_RF + (WRITE && !BF ? 8 * 128 * 4 : 0);  // read: 32 rows of 64 bytes for each epilogue warp
     static constexpr int OFF_BAR = OFF_OUT + (WRITE ? 0 : NE * 2048);
     static constexpr int USED = OFF_BAR + 256;
     static constexpr int SMEM = (USED > 120 * 1024 ? USED : 120 * 1024) + 1024;
@@ -105,13 +111,13 @@ __device__ __forceinline__ long long row_of(const PagedCodecParams& P, long long
 }  // namespace ctc
 
 // The parts both directions share: barriers, tensor memory, R_s.  BODY: see the two kernels.
-template <int D, bool WRITE>
+template <int D, bool WRITE, int DT>
 struct CtcCommon {
-    using C = ctc::Cfg<D, WRITE>;
+    using C = ctc::Cfg<D, WRITE, DT>;
     static constexpr int A_FULL = 0, A_EMPTY = C::ST, ACC_FULL = 2 * C::ST, ACC_EMPTY = 2 * C::ST + C::NACC,
                          N_BARS = 2 * C::ST + 2 * C::NACC;
 
-    // R_s rows: write [n][x] hi and lo (K-major B: rows are the outputs n0 .. n0 + NB - 1); read [n][x] with the
+    // R_s rows: write [n][x] in its parts (K-major B: rows are the outputs n0 .. n0 + NB - 1); read [n][x] with the
     // rows in the order of dq_kperm (MN-major B: rows are the contraction index)
     static __device__ void setup(uint8_t* smem, uint64_t* bars, uint32_t* slot, int warp, const uint32_t* sign, bool srht,
                                  int n0) {
@@ -141,11 +147,28 @@ struct CtcCommon {
         constexpr int ROWS = WRITE ? C::NB : D;
         for (int c = threadIdx.x; c < ROWS * (D / 8); c += blockDim.x) {
             const int r = c / (D / 8), ch = c % (D / 8);
-            uint4 hi, lo;
             uint8_t* at = smem + (ch >> 3) * (ROWS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-            tile::r_chunk<D, WRITE, WRITE ? ctc::kUp : 0>(WRITE ? n0 + r : dq_kperm(r), 8 * ch, srht, tw, sg, hi, lo);
-            *reinterpret_cast<uint4*>(at) = hi;
-            if constexpr (WRITE) *reinterpret_cast<uint4*>(at + ROWS * D * 2) = lo;
+            if constexpr (C::BF) {
+                float f[8];
+                tile::r_entries<D, 0>(n0 + r, 8 * ch, srht, tw, sg, f);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+                        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+                        f[2 * j] -= __uint_as_float(w[j] << 16);
+                        f[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+                    }
+                    *reinterpret_cast<uint4*>(at + k * ROWS * D * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else {
+                uint4 hi, lo;
+                tile::r_chunk<D, WRITE, C::UP>(WRITE ? n0 + r : dq_kperm(r), 8 * ch, srht, tw, sg, hi, lo);
+                *reinterpret_cast<uint4*>(at) = hi;
+                if constexpr (WRITE) *reinterpret_cast<uint4*>(at + ROWS * D * 2) = lo;
+            }
         }
         ptx::fence_proxy_async_smem();
         __syncthreads();
@@ -154,8 +177,9 @@ struct CtcCommon {
 
 // DT: SRFTKV_DTYPE_*
 template <int D, int DT>
-__global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_tc_kernel(const __grid_constant__ PagedCodecParams P) {
-    using S = CtcCommon<D, true>;
+__global__ void __launch_bounds__(ctc::Cfg<D, true, DT>::THREADS, 1) paged_quantize_tc_kernel(const __grid_constant__ PagedCodecParams P) {
+    using S = CtcCommon<D, true, DT>;
+    constexpr bool CONVERT = DT == SRFTKV_DTYPE_BF16 && !S::C::BF;  // bf16 rows go over to fp16
     using C = typename S::C;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -211,14 +235,14 @@ __global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_
                 failed = true;
                 break;
             }
-            if constexpr (!C::AHEAD || DT == SRFTKV_DTYPE_BF16) {
+            if constexpr (!C::AHEAD || CONVERT) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     const int r = 16 * warp + i * RPS + lane / LPR;
                     uint4* at = reinterpret_cast<uint4*>(smem + piece(s, r));
                     const uint4 q = C::AHEAD ? *at : v[C::AHEAD ? 0 : i];
                     uint32_t w[4] = {q.x, q.y, q.z, q.w};
-                    if constexpr (DT == SRFTKV_DTYPE_BF16) {
+                    if constexpr (CONVERT) {
                         // exponents of this lane's values, two a word; rows whose largest lies in [2^-6, 2^15) go over as
                         // they are (an error of 2^-25 at most), others by the power of two that brings it to [1, 2)
                         uint32_t m2 = 0;
@@ -261,9 +285,9 @@ __global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_
         }
         if constexpr (C::AHEAD) ctc::wait_copies<0>();  // (after a wait that ran out some are under way)
     } else if (warp < C::MMA) {
-        // a warp: lanes 32 quarter .., 32 columns; where a tile has fewer than four such columns, the warps left over take
-        // every other tile
-        constexpr int UNITS = C::NB / 32, GROUPS = C::NE / 4 / UNITS;
+        // a warp: lanes 32 quarter .., a unit of 32 columns or more of them in turn; where a tile has fewer units than
+        // there are warps, those left over take every other tile
+        constexpr int UNITS = C::NB / 32, PER = C::NE / 4, GROUPS = PER > UNITS ? PER / UNITS : 1;
         const int quarter = warp & 3, unit = ((warp - C::NL) >> 2) % UNITS, group = ((warp - C::NL) >> 2) / UNITS;
         auto slot_at = [&](int u) { return u < total ? ctc::slot_of(P, ctc::tile_at(P, u, per_side).t0 + 32 * quarter + lane) : -1ll; };
         int i_tile = group;
@@ -280,9 +304,9 @@ __global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_
                 break;
             }
             tc::fence_after_sync();
-            const float up = DT == SRFTKV_DTYPE_BF16 ? rf[(i_tile & 7) * 128 + r] : 1.f;
-            {
-                const int c0 = 32 * unit;
+            const float up = CONVERT ? rf[(i_tile & 7) * 128 + r] : 1.f;
+#pragma unroll 1
+            for (int c0 = 32 * unit; c0 < C::NB; c0 += 32 * (PER < UNITS ? PER : UNITS)) {
                 uint32_t raw[32];
                 tc::ld_32x32b_x32(tmem + ((uint32_t)(32 * quarter) << 16) + a * C::NB + c0, raw);
                 tc::wait_ld(raw);
@@ -294,7 +318,7 @@ __global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_
                     float z[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(raw[j]);
-                    if (DT == SRFTKV_DTYPE_BF16 && up != 1.f) {
+                    if (CONVERT && up != 1.f) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) z[j] *= up;
                     }
@@ -311,9 +335,9 @@ __global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_
                     uint8_t* crow = sd.codes + row * (D * sd.bits / 8) + col * sd.bits / 8;
                     auto put = [&](auto bits) {
                         constexpr int B = decltype(bits)::value;
-                        if (sd.sfmt == SRFTKV_SCALE_FP32) quant_store_row<32, B, SRFTKV_SCALE_FP32, ctc::kUp>(z, P.group, crow, srow);
-                        else if (sd.sfmt == SRFTKV_SCALE_FP16) quant_store_row<32, B, SRFTKV_SCALE_FP16, ctc::kUp>(z, P.group, crow, srow);
-                        else quant_store_row<32, B, SRFTKV_SCALE_E8M0, ctc::kUp>(z, P.group, crow, srow);
+                        if (sd.sfmt == SRFTKV_SCALE_FP32) quant_store_row<32, B, SRFTKV_SCALE_FP32, C::UP>(z, P.group, crow, srow);
+                        else if (sd.sfmt == SRFTKV_SCALE_FP16) quant_store_row<32, B, SRFTKV_SCALE_FP16, C::UP>(z, P.group, crow, srow);
+                        else quant_store_row<32, B, SRFTKV_SCALE_E8M0, C::UP>(z, P.group, crow, srow);
                     };
                     if (sd.bits == 4) put(std::integral_constant<int, 4>{});
                     else put(std::integral_constant<int, 8>{});
@@ -335,14 +359,14 @@ __global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_
             tc::fence_after_sync();
             if (one) {
                 const uint32_t ao = tile::desc_k(sbase + C::OFF_A + s * C::A_BYTES), bo = tile::desc_k(sbase), dst = tmem + a * C::NB;
-                // lo first: an accumulation rounds to the size of the sum so far, which lo leaves small, so only the D/16
-                // steps of hi count
+                // the smallest part first: an accumulation rounds to the size of the sum so far, which that leaves small,
+                // so only the D/16 steps of the largest count
+                constexpr uint32_t idesc = tile::idesc(128, C::NB, false) | (C::BF ? 1u << 7 | 1u << 10 : 0u);  // (A, B bf16)
 #pragma unroll
-                for (int ks = 0; ks < 2 * (D / 16); ++ks) {
-                    const int k = ks % (D / 16);
+                for (int ks = 0; ks < C::PARTS * (D / 16); ++ks) {
+                    const int k = ks % (D / 16), part = C::PARTS - 1 - ks / (D / 16);
                     const uint32_t as = (k >> 2) * 1024 + (k & 3) * 2, bs = (k >> 2) * (C::NB * 8) + (k & 3) * 2;
-                    tc::mma_f16(dst, tile::desc(ao + as), tile::desc(bo + bs + (ks < D / 16 ? C::NB * D / 8 : 0)),
-                                tile::idesc(128, C::NB, false), ks > 0);
+                    tc::mma_f16(dst, tile::desc(ao + as), tile::desc(bo + bs + part * (C::NB * D / 8)), idesc, ks > 0);
                 }
                 tc::commit(bar(S::A_EMPTY + s));
                 tc::commit(bar(S::ACC_FULL + a));
@@ -358,8 +382,8 @@ __global__ void __launch_bounds__(ctc::Cfg<D, true>::THREADS, 1) paged_quantize_
 }
 
 template <int D, int DT>
-__global__ void __launch_bounds__(ctc::Cfg<D, false>::THREADS, 1) paged_dequantize_tc_kernel(const __grid_constant__ PagedCodecParams P) {
-    using S = CtcCommon<D, false>;
+__global__ void __launch_bounds__(ctc::Cfg<D, false, DT>::THREADS, 1) paged_dequantize_tc_kernel(const __grid_constant__ PagedCodecParams P) {
+    using S = CtcCommon<D, false, DT>;
     using C = typename S::C;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -569,12 +593,13 @@ __global__ void __launch_bounds__(ctc::Cfg<D, false>::THREADS, 1) paged_dequanti
 
 template <int D>
 static int launch_codec_tc(const PagedCodecParams& P, int dtype, bool write, cudaStream_t stream) {
-    using CW = ctc::Cfg<D, true>;
-    using CR = ctc::Cfg<D, false>;
+    using CW = ctc::Cfg<D, true, SRFTKV_DTYPE_FP16>;
+    using CB = ctc::Cfg<D, true, SRFTKV_DTYPE_BF16>;
+    using CR = ctc::Cfg<D, false, SRFTKV_DTYPE_FP16>;
     void (*k)(PagedCodecParams) =
         write ? (dtype == SRFTKV_DTYPE_BF16 ? paged_quantize_tc_kernel<D, SRFTKV_DTYPE_BF16> : paged_quantize_tc_kernel<D, SRFTKV_DTYPE_FP16>)
               : (dtype == SRFTKV_DTYPE_BF16 ? paged_dequantize_tc_kernel<D, SRFTKV_DTYPE_BF16> : paged_dequantize_tc_kernel<D, SRFTKV_DTYPE_FP16>);
-    const int smem = write ? CW::SMEM : CR::SMEM, split = write ? CW::NSPLIT : 1;
+    const int smem = !write ? CR::SMEM : dtype == SRFTKV_DTYPE_BF16 ? CB::SMEM : CW::SMEM, split = write ? CW::NSPLIT : 1;
     const int total = (P.n_tokens + 127) / 128 * P.H * P.n_sides, sms = device_sm_count();
     const int ctas = total < sms / split ? total : sms / split;
     static std::atomic<unsigned long long> done[4];
