@@ -8,7 +8,7 @@
 // group_scale's and the magic-number FMA's of the contiguous codec, so a page
 // holds the bytes the contiguous call would store for the same z.
 //
-// One warp a row (paged_rotate.cuh).
+// One warp a row (paged_rotate.cuh) here; many rows on the tensor cores (paged_codec_tc.cuh).
 #include "codec_impl.cuh"
 #include "paged.h"
 #include "paged_rotate.cuh"
@@ -171,8 +171,8 @@ static int launch(const PagedCodecCall& c, bool quantize) {
     P.div_shift = div.shift;
     // Many rows: the tensor cores, which every CTA first builds R_s for (10 us a call at d = 128, 6 at 64, 19 to 30 at
     // 256); few: one warp a row (d = 128: 8.8 us at 8192 rows, 14.3 at 16384 against 10 here; d = 64: 5.9 and 9.4 against
-    // 5.6; d = 256: 20 and 36 at 16384 and 32768, against 25 at both written and 34 read back).  The write's epilogue holds 32 columns a thread, so its groups end there; both sides rotate
-    // with one R_s.
+    // 5.6; d = 256: 20 and 36 at 16384 and 32768, against 25 at both written and 34 read back).  The write's epilogue
+    // holds 32 columns a thread, so its groups end there; both sides rotate with one R_s.
     const long long rows = (long long)P.n_tokens * P.H * P.n_sides;
     const bool one_r = P.n_sides == 1 || P.side[0].transform == P.side[1].transform;
     if (rows >= (c.d < 256 ? 10240 : quantize ? 20480 : 28672) && one_r && (!quantize || P.group <= 32)) {
