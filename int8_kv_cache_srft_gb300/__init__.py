@@ -324,6 +324,8 @@ def _rows_arg(fn: str, name: str, x: torch.Tensor, n: int, H: int, d: int, dtype
     s0, s1, s2 = x.stride()
     if n * H and (s2 != 1 or (s1 != d and H > 1)):
         _invalid(fn, f"{name} must have its last two dimensions dense (strides {tuple(x.stride())})")
+    if n > 1 and H and s0 < H * d:  # (0, an expanded tensor's, would mean dense rows to the library)
+        _invalid(fn, f"{name}'s rows must not overlap (strides {tuple(x.stride())})")
     if x.device != device:
         _invalid(fn, f"{name} must be on the pools' device")
     return s0 if n > 1 else 0

@@ -564,6 +564,39 @@ def test_two_streams_at_once():
         assert torch.equal(o, want[i % 2])
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_large_calls_on_two_streams_at_once(d):
+    """Prompts on one stream beside a large write and read on the other: the same bits as one after the other."""
+    H, n = 2, 16000
+    c = R.Cache(K, [900, 400], H, d, 4, 4, 16, "fp16", 16, BF16)
+    q, b = rand(1300, 4 * H, d, dtype=BF16, seed=3), c.batch(K, [900, 400])
+    want = R.attend(K, c, q, b)
+    pools = [K.alloc_pages(n // 32, 32, H, d, 8, 16, scale_format="e8m0") for _ in range(2)]
+    x = [rand(n, H, d, dtype=BF16, seed=s) for s in (5, 6)]
+    y = [torch.zeros_like(a) for a in x]
+    slots = torch.randperm(n, device="cuda")
+
+    def codec():
+        K.srft_kv_quantize_paged(pools[0], x[0], pools[1], x[1], slots, 7)
+        K.srft_kv_dequantize_paged(pools[0], y[0], pools[1], y[1], slots, 7)
+
+    codec()
+    torch.cuda.synchronize()
+    kept = [a.clone() for a in y] + [p.codes.clone() for p in pools]
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for a in y + [p.codes for p in pools]:
+        a.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(streams[0]):
+            outs.append(R.attend(K, c, q, b))
+        with torch.cuda.stream(streams[1]):
+            codec()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    assert all(torch.equal(a, k) for a, k in zip(y + [p.codes for p in pools], kept))
+
+
 def test_stream_argument():
     """Work goes to the stream given, not the current one."""
     c = R.Cache(K, [100], 1, 64, 4, 4, 16, "fp32", 16, HALF)

@@ -128,3 +128,8 @@ def test_binding_checks_tensors():
         K.q4kv_paged_attention(x.float(), x, p, p, K.PagedBatch(t, n), 0.0, 0, 1, c)
     with pytest.raises(K.SrftKvError):  # a side without its rows
         K.srft_kv_quantize_paged(p, None, None, None, slots, 1)
+    with pytest.raises(K.SrftKvError, match="overlap"):  # one row for all tokens: its stride is 0
+        K.srft_kv_quantize_paged(p, x[:1].expand(3, 2, 128), None, None, slots, 1)
+    one = torch.zeros(1, 2, 128, dtype=torch.float16)
+    with pytest.raises(K.SrftKvError, match="overlap"):
+        K.q4kv_paged_attention(one.expand(3, 2, 128), x, p, p, K.PagedBatch(t, n), 0.0, 0, 1, c)
