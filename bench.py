@@ -92,7 +92,7 @@ KERNEL_SOURCES = {  # (api.cu encodes the tensor maps, whose L2 promotion affect
                                 "srft_math.cuh", "ptx.cuh", "api.cu"),
     "srft_dequantize_tc_kernel": ("codec_tc.cu", "codec_tc_common.cuh", "codec_impl.cuh", "tcgen05.cuh",
                                   "srft_math.cuh", "ptx.cuh", "api.cu"),
-    "q4kv_attn_split_kernel": ("attention.cu", "ptx.cuh", "srft_math.cuh", "api.cu"),
+    "q4kv_attn_split_kernel": ("attention.cu", "attn_frag.cuh", "ptx.cuh", "srft_math.cuh", "api.cu"),
 }
 
 
