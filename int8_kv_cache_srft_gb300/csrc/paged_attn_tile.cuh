@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
             tc::commit(bar(ROT));
         }
         __syncwarp();
-        if (!ptx::mbar_spin_bounded(bar(ROT), nh & 1)) failed = true;
+        if (!__all_sync(0xffffffffu, ptx::mbar_spin_bounded(bar(ROT), nh & 1))) failed = true;  // (a warp's lanes alike)
         tc::fence_after_sync();
         __syncthreads();
     }
@@ -816,7 +816,11 @@ __global__ void __launch_bounds__(tile::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(R_FULL));
             }
+        } else if (W.n_parts == 1 && W.images) {
+            ptx::named_bar_sync(1, 256);  // (a warp whose wait ran out meets the others there all the same)
         }
+        } else if (W.n_parts == 1 && W.images) {
+            ptx::named_bar_sync(1, 256);
         }
     } else if (!failed && warp == 16) {
         // =========================== MMA ===========================
